@@ -1,16 +1,20 @@
 """Compile the CUDA library (kernels + C ABI) for sm_103a, in-tree.
 
 The output is ``host_offload_serving_gb300/_build/libhisparse.so``; it is
-rebuilt when ``csrc/hisparse.cu`` or ``include/hisparse.h`` is newer.
+rebuilt when a source under ``csrc/`` or ``include/hisparse.h`` is newer.  The
+translation units are compiled side by side and linked.
 """
+import glob
 import os
 import shutil
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "hisparse.cu")
-HDR = os.path.join(ROOT, "include", "hisparse.h")
+CSRC = os.path.join(PKG, "csrc")
+SRCS = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+HDRS = [os.path.join(ROOT, "include", "hisparse.h"), *sorted(glob.glob(os.path.join(CSRC, "*.cuh")))]
 OUT = os.path.join(PKG, "_build", "libhisparse.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -26,19 +30,34 @@ def up_to_date():
     if not os.path.exists(OUT):
         return False
     t = os.path.getmtime(OUT)
-    return all(os.path.getmtime(p) <= t for p in (SRC, HDR, __file__))
+    return all(os.path.getmtime(p) <= t for p in (*SRCS, *HDRS, __file__))
 
 
 def build(force=False, verbose=False):
     if not force and up_to_date():
         return OUT
     os.makedirs(os.path.dirname(OUT), exist_ok=True)
-    tmp = OUT + f".{os.getpid()}.tmp"
-    cmd = [nvcc(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-           "-I", os.path.join(ROOT, "include"), "-o", tmp, SRC]
+    exe = nvcc()
+    tag = f".{os.getpid()}.tmp"
+    flags = [*ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
+             "-I", os.path.join(ROOT, "include")]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
-    os.replace(tmp, OUT)
+        flags.insert(0, "-Xptxas=-v")
+
+    def compile_one(src):
+        obj = os.path.join(PKG, "_build", os.path.basename(src) + tag + ".o")
+        cmd = [exe, *flags, "-c", "-o", obj, src]
+        if verbose:
+            print(" ".join(cmd))
+        subprocess.check_call(cmd)
+        return obj
+
+    with ThreadPoolExecutor(len(SRCS)) as ex:
+        objs = list(ex.map(compile_one, SRCS))
+    try:
+        subprocess.check_call([exe, *ARCH, "-shared", "-o", OUT + tag, *objs])
+        os.replace(OUT + tag, OUT)
+    finally:
+        for o in objs:
+            os.remove(o)
     return OUT

@@ -49,7 +49,10 @@
 #include <thread>
 #include <vector>
 
+#include "common.cuh"
 #include "hisparse.h"
+
+thread_local int g_last_cuda_error = 0;
 
 namespace {
 
@@ -60,8 +63,6 @@ constexpr int32_t kUnresolved = INT32_MIN;
 constexpr uint32_t kAlias = 1u << 30;  // a victim entry of a repeated miss (union mode): not fetched
 constexpr unsigned kFull = 0xffffffffu;
 static_assert(kWarps == 32, "warp-total scan assumes 32 warps");
-
-thread_local int g_last_cuda_error = 0;
 
 // ---------------------------------------------------------------------------
 // Shared-memory layout of a resolve CTA (identical on host and device).
@@ -1959,18 +1960,6 @@ struct hisparse_handle {
 };
 
 namespace {
-
-int cuda_fail(cudaError_t e) {
-  g_last_cuda_error = static_cast<int>(e);
-  return HISPARSE_ECUDA;
-}
-#define HS_CUDA(call)                              \
-  do {                                             \
-    cudaError_t e_ = (call);                       \
-    if (e_ != cudaSuccess) return cuda_fail(e_);   \
-  } while (0)
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int layer_ok(const hisparse_handle *h, int32_t layer) {
   if (!h || layer < 0 || layer >= h->L) return HISPARSE_EINVAL;

@@ -1,0 +1,487 @@
+// pages.cu -- the pages of the resident tier: grow, fork, free and compact
+// (hisparse_pages_* of include/hisparse.h).
+//
+// Two launches at most.  A plan kernel (one cluster of kPlanCtas CTAs) settles which
+// pages go where: each CTA scans a slice of the reference counts, the slices' totals
+// meet in distributed shared memory, and every rank below is the exact rank in
+// page order or list order, so results depend on no timing.  Then a copy kernel
+// over the whole GPU moves the bytes of the pages in the plan.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int kPlanCtas = 8;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+// d_work: word 0 the number of copies, word 1 the pages in use; then three arrays of `span`
+// = max(num_pages, num_requests) words: the pages copied from, the pages copied to,
+// and the rows of each copy (fork) or where each page moved (compact).  With
+// grow and fork the third array first holds the list's demands, and the second the free
+// pages by rank.
+constexpr int kWorkHead = 16;
+
+struct PoolArgs {
+  int32_t pages, R, blocks, page_tokens, layers;
+  int64_t row_bytes, layer_stride, page_stride;
+  char *store;
+  int32_t *tables, *refs, *work;
+  uint32_t *status;
+  int32_t span, n;
+  const int32_t *src, *dst, *want;  // fork: tokens in want; grow: blocks in want
+};
+
+__device__ __forceinline__ void report(const PoolArgs &a, uint32_t bit) {
+  if (a.status) atomicOr(a.status, bit);
+}
+
+// Sum over the CTA and this thread's exclusive prefix; all threads call it.
+__device__ __forceinline__ int block_scan(int v, int *warp_sums, int &total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[w] = x;
+  __syncthreads();
+  const int s = warp_sums[lane];  // kPlanWarps == 32
+  int t = s;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) t += y;
+  }
+  total = __shfl_sync(0xffffffffu, t, 31);
+  const int before = __shfl_sync(0xffffffffu, t - s, w);
+  return before + x - v;
+}
+
+// Every CTA of the cluster learns the totals of all CTAs: returns the sum of
+// the lower ranks' and, in `all`, of all.
+__device__ __forceinline__ int cluster_scan(int mine, int *slot, int &all) {
+  cg::cluster_group c = cg::this_cluster();
+  const int rank = c.block_rank();
+  if (threadIdx.x < kPlanCtas) *c.map_shared_rank(slot + rank, threadIdx.x) = mine;
+  c.sync();
+  int before = 0;
+  all = 0;
+  for (int i = 0; i < kPlanCtas; ++i) {
+    if (i < rank) before += slot[i];
+    all += slot[i];
+  }
+  return before;
+}
+
+struct Slice {
+  int lo, hi;
+};
+__device__ __forceinline__ Slice slice_of(int total, int rank) {
+  const int per = ((total + kPlanCtas - 1) / kPlanCtas + 3) & ~3;
+  const int lo = min(total, rank * per);
+  return {lo, min(total, lo + per)};
+}
+
+// The page a thread scans in one turn of a slice: 4 in a row, -1 past the end.
+__device__ __forceinline__ int4 refs_at(const PoolArgs &a, int p, int hi) {
+  int4 r = make_int4(-1, -1, -1, -1);
+  if (p + 3 < hi) return *reinterpret_cast<const int4 *>(a.refs + p);
+  if (p < hi) r.x = a.refs[p];
+  if (p + 1 < hi) r.y = a.refs[p + 1];
+  if (p + 2 < hi) r.z = a.refs[p + 2];
+  return r;
+}
+
+// The free pages of rank 0 .. need-1 into list[rank].  Returns how many are free
+// (at least `need`, or all there are).
+__device__ int find_free(const PoolArgs &a, int need, int *list, int *warp_sums, int *slot) {
+  const int rank = cg::this_cluster().block_rank();
+  const Slice s = slice_of(a.pages, rank);
+  int count = 0;
+  for (int p = s.lo + 4 * threadIdx.x; p < s.hi; p += 4 * kPlanThreads) {
+    const int4 r = refs_at(a, p, s.hi);
+    count += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+  }
+  int total, all;
+  block_scan(count, warp_sums, total);
+  int base = cluster_scan(total, slot, all);
+  for (int p0 = s.lo; p0 < s.hi && base < need; p0 += 4 * kPlanThreads) {
+    const int p = p0 + 4 * threadIdx.x;
+    const int4 r = refs_at(a, p, s.hi);
+    const int f = (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+    int k = base + block_scan(f, warp_sums, total);
+    const int v[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (v[i] == 0) {
+        if (k < need) list[k] = p + i;
+        ++k;
+      }
+    base += total;
+  }
+  return all;
+}
+
+// ---------------------------------------------------------------------------
+// Grow and fork.  Demands of the list's entries -> ranks -> free pages -> tables.
+// ---------------------------------------------------------------------------
+struct ForkNeed {
+  bool ok;
+  int full, part, last;  // shared blocks, rows of the part-filled one, its page (-1: none)
+};
+__device__ __forceinline__ ForkNeed fork_need(const PoolArgs &a, int i) {
+  ForkNeed f = {false, 0, 0, -1};
+  const int s = a.src[i], d = a.dst[i], t = a.want[i];
+  if (s < 0 || s >= a.R || d < 0 || d >= a.R || t < 0) return f;
+  f.full = t / a.page_tokens;
+  f.part = t - f.full * a.page_tokens;
+  if (f.full > a.blocks || (f.full == a.blocks && f.part)) return f;
+  f.ok = true;
+  if (f.part) f.last = a.tables[static_cast<int64_t>(s) * a.blocks + f.full];
+  return f;
+}
+
+template <bool kFork>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
+  __shared__ int warp_sums[32], slot[kPlanCtas];
+  pdl_wait();
+  pdl_launch();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), lane = threadIdx.x & 31;
+  const int gwarp = (rank * kPlanThreads + threadIdx.x) >> 5;
+  constexpr int kGWarps = kPlanCtas * kPlanWarps;
+  int32_t *from = a.work + kWorkHead, *to = from + a.span, *third = to + a.span;
+
+  // demand of each entry; INT_MIN marks one that is skipped
+  for (int i = gwarp; i < a.n; i += kGWarps) {
+    int need = INT_MIN;
+    if (kFork) {
+      const ForkNeed f = fork_need(a, i);
+      bool empty = f.ok;
+      if (f.ok) {
+        const int32_t *row = a.tables + static_cast<int64_t>(a.dst[i]) * a.blocks;
+        for (int b = lane; b < a.blocks; b += 32) empty &= row[b] == -1;
+      }
+      if (__all_sync(0xffffffffu, empty)) need = f.last >= 0 ? 1 : 0;
+    } else {
+      const int r = a.src[i], w = a.want[i];
+      if (r >= 0 && r < a.R && w >= 0 && w <= a.blocks) {
+        const int32_t *row = a.tables + static_cast<int64_t>(r) * a.blocks;
+        int k = 0;
+        for (int b = lane; b < w; b += 32) k += row[b] == -1;
+        need = __reduce_add_sync(0xffffffffu, k);
+      }
+    }
+    if (lane == 0) {
+      third[i] = need;
+      if (need == INT_MIN) report(a, HISPARSE_ERR_RANGE);
+    }
+  }
+  cluster.sync();
+  // every CTA ranks the whole list: thread t takes a run of entries
+  const int run = (a.n + kPlanThreads - 1) / kPlanThreads;
+  const int i0 = min(a.n, static_cast<int>(threadIdx.x) * run), i1 = min(a.n, i0 + run);
+  int mine = 0;
+  for (int i = i0; i < i1; ++i) mine += max(0, third[i]);
+  int demand;
+  int at = block_scan(mine, warp_sums, demand);
+  const int free_pages = find_free(a, min(demand, a.pages), to, warp_sums, slot);
+  // the demands that fit are a prefix of the list; `from` keeps each entry's first rank
+  for (int i = i0; i < i1; ++i) {
+    const int need = max(0, third[i]);
+    if (rank == 0) from[i] = need > 0 && at + need > free_pages ? -1 : at;
+    at += need;
+  }
+  cluster.sync();  // the free list, the ranks; everyone has read every demand
+  if (kFork) {
+    for (int i = gwarp; i < a.n; i += kGWarps) {
+      const int need = third[i], r0 = from[i];
+      int rows = 0, last = -1;
+      if (need >= 0 && r0 >= 0) {
+        const ForkNeed f = fork_need(a, i);
+        const int32_t *src = a.tables + static_cast<int64_t>(a.src[i]) * a.blocks;
+        int32_t *dst = a.tables + static_cast<int64_t>(a.dst[i]) * a.blocks;
+        for (int b = lane; b < f.full; b += 32) {
+          const int p = src[b];
+          if (p >= 0 && p < a.pages) {
+            dst[b] = p;
+            atomicAdd(a.refs + p, 1);
+          } else if (p != -1) {
+            report(a, HISPARSE_ERR_RANGE);
+          }
+        }
+        if (need && f.last >= a.pages) {
+          report(a, HISPARSE_ERR_RANGE);
+        } else if (need) {
+          rows = f.part;
+          last = f.last;
+          if (lane == 0) {
+            dst[f.full] = to[r0];
+            a.refs[to[r0]] = 1;
+          }
+        }
+      } else if (need >= 0 && lane == 0) {
+        report(a, HISPARSE_ERR_FULL);
+      }
+      __syncwarp();
+      // copy i: `rows` rows (0: none) of page `last`
+      if (lane == 0) {
+        third[i] = rows;
+        from[i] = last;
+      }
+    }
+  } else {
+    for (int i = gwarp; i < a.n; i += kGWarps) {
+      const int need = third[i];
+      int r = from[i];
+      if (need <= 0) continue;
+      if (r < 0) {
+        if (lane == 0) report(a, HISPARSE_ERR_FULL);
+        continue;
+      }
+      int32_t *row = a.tables + static_cast<int64_t>(a.src[i]) * a.blocks;
+      for (int b0 = 0; b0 < a.want[i]; b0 += 32) {
+        const int b = b0 + lane;
+        const bool hole = b < a.want[i] && row[b] == -1;
+        const unsigned m = __ballot_sync(0xffffffffu, hole);
+        if (hole) {
+          const int p = to[r + __popc(m & ((1u << lane) - 1))];
+          row[b] = p;
+          a.refs[p] = 1;
+        }
+        r += __popc(m);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Compact: with m pages in use, the j-th page in use at or above m moves to
+// the j-th free page below m.  Rank of a free page p < m: p - used before p;
+// of a mover p >= m: used before p - used before m.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PoolArgs a) {
+  __shared__ int warp_sums[32], slot[kPlanCtas], slot2[kPlanCtas];
+  pdl_wait();
+  pdl_launch();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank();
+  int32_t *from = a.work + kWorkHead, *to = from + a.span, *moved = to + a.span;
+  const Slice s = slice_of(a.pages, rank);
+  int count = 0, total, m, low;
+  cluster.sync();  // every CTA of the cluster runs: its shared memory may be written
+  for (int p = s.lo + 4 * threadIdx.x; p < s.hi; p += 4 * kPlanThreads) {
+    const int4 r = refs_at(a, p, s.hi);
+    count += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
+  }
+  block_scan(count, warp_sums, total);
+  const int before = cluster_scan(total, slot, m);
+  // used pages below m
+  count = 0;
+  for (int p = s.lo + 4 * threadIdx.x; p < min(s.hi, m); p += 4 * kPlanThreads) {
+    const int4 r = refs_at(a, p, s.hi);
+    const int v[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) count += v[i] > 0 && p + i < m;
+  }
+  block_scan(count, warp_sums, total);
+  cluster_scan(total, slot2, low);
+  int base = before;
+  for (int p0 = s.lo; p0 < s.hi; p0 += 4 * kPlanThreads) {
+    const int p = p0 + 4 * threadIdx.x;
+    const int4 r = refs_at(a, p, s.hi);
+    const int v[4] = {r.x, r.y, r.z, r.w};
+    int used = base + block_scan((r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0), warp_sums, total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (p + i >= s.hi) break;
+      if (v[i] > 0) {
+        if (p + i >= m) from[used - low] = p + i;
+        ++used;
+      } else if (p + i < m) {
+        to[p + i - used] = p + i;
+      }
+    }
+    base += total;
+  }
+  cluster.sync();
+  const int movers = m - low;
+  for (int j = rank * kPlanThreads + threadIdx.x; j < movers; j += kPlanCtas * kPlanThreads) {
+    const int f = from[j], t = to[j];
+    moved[f] = t;
+    a.refs[t] = a.refs[f];
+    a.refs[f] = 0;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    a.work[0] = movers;
+    a.work[1] = m;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// page_copy_kernel: the bytes of the plan's pages in every layer, in 16-byte
+// chunks over the whole grid, kUnroll reads of a thread in flight.  For a
+// fork, copy i goes to the part-filled block of its destination's table row.  For a
+// compaction the table entries above the used pages follow their pages too.
+// ---------------------------------------------------------------------------
+constexpr int kCopyThreads = 512;
+constexpr int kCopyUnroll = 8;
+
+template <bool kFork>
+__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const PoolArgs a) {
+  pdl_wait();
+  pdl_launch();
+  const int32_t *from = a.work + kWorkHead, *to = from + a.span, *third = to + a.span;
+  const int copies = kFork ? a.n : a.work[0];
+  const int64_t tid = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kCopyThreads;
+  if (!kFork) {
+    const int m = a.work[1];
+    for (int64_t e = tid; e < static_cast<int64_t>(a.R) * a.blocks; e += step) {
+      const int p = a.tables[e];
+      if (p < m) continue;
+      const int t = p < a.pages ? third[p] : -1;
+      if (t >= 0 && t < m) {
+        a.tables[e] = t;
+      } else {
+        report(a, HISPARSE_ERR_RANGE);  // an entry that no count stands for
+      }
+    }
+  }
+  // one CTA to a (copy, layer) pair in turn
+  const int64_t items = static_cast<int64_t>(copies) * a.layers;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int c = static_cast<int>(it / a.layers), l = static_cast<int>(it - static_cast<int64_t>(c) * a.layers);
+    int rows = a.page_tokens, dst;
+    if (kFork) {
+      rows = third[c];
+      if (rows == 0) continue;
+      dst = a.tables[static_cast<int64_t>(a.dst[c]) * a.blocks + a.want[c] / a.page_tokens];
+      if (dst < 0 || dst >= a.pages) continue;
+    } else {
+      dst = to[c];
+    }
+    const uint4 *s = reinterpret_cast<const uint4 *>(a.store + l * a.layer_stride +
+                                                     static_cast<int64_t>(from[c]) * a.page_stride);
+    uint4 *d = reinterpret_cast<uint4 *>(a.store + l * a.layer_stride +
+                                         static_cast<int64_t>(dst) * a.page_stride);
+    const int64_t chunks = rows * a.row_bytes / 16;
+    for (int64_t i = threadIdx.x; i < chunks; i += kCopyThreads * kCopyUnroll) {
+      uint4 v[kCopyUnroll];
+#pragma unroll
+      for (int u = 0; u < kCopyUnroll; ++u)
+        if (i + u * kCopyThreads < chunks) v[u] = s[i + u * kCopyThreads];
+#pragma unroll
+      for (int u = 0; u < kCopyUnroll; ++u)
+        if (i + u * kCopyThreads < chunks) d[i + u * kCopyThreads] = v[u];
+    }
+  }
+}
+
+// Each entry of the listed rows is taken out once, whatever the list repeats.
+__global__ void __launch_bounds__(256) free_kernel(const PoolArgs a) {
+  pdl_wait();
+  pdl_launch();
+  const int r = a.src[blockIdx.x];
+  if (r < 0 || r >= a.R) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) report(a, HISPARSE_ERR_RANGE);
+    return;
+  }
+  int32_t *row = a.tables + static_cast<int64_t>(r) * a.blocks;
+  for (int b = blockIdx.y * 256 + threadIdx.x; b < a.blocks; b += gridDim.y * 256) {
+    if (row[b] == -1) continue;
+    const int p = atomicExch(row + b, -1);
+    if (p == -1) continue;
+    if (p < 0 || p >= a.pages) {
+      report(a, HISPARSE_ERR_RANGE);
+    } else {
+      atomicSub(a.refs + p, 1);
+    }
+  }
+}
+
+int pool_args(const hisparse_page_pool *p, PoolArgs &a) {
+  if (!p || p->num_pages < 1 || p->num_requests < 1 || p->max_blocks < 1 || p->page_tokens < 1 ||
+      p->layers < 1 || p->row_bytes < 16 || p->row_bytes % 16)
+    return HISPARSE_EINVAL;
+  if (!p->store || !p->d_tables || !p->d_refs || !p->d_work || !aligned16(p->store) ||
+      !aligned16(p->d_refs) || p->layer_stride % 16 || p->page_stride % 16 ||
+      p->page_stride < p->row_bytes * p->page_tokens || p->layer_stride < 0)
+    return HISPARSE_EINVAL;
+  if (p->num_pages > (1 << 30) || p->num_requests > 8192) return HISPARSE_EBOUND;
+  a = {};
+  a.pages = p->num_pages; a.R = p->num_requests; a.blocks = p->max_blocks;
+  a.page_tokens = p->page_tokens; a.layers = p->layers;
+  a.row_bytes = p->row_bytes; a.layer_stride = p->layer_stride; a.page_stride = p->page_stride;
+  a.store = static_cast<char *>(p->store);
+  a.tables = p->d_tables; a.refs = p->d_refs; a.work = p->d_work; a.status = p->d_status;
+  a.span = std::max(a.pages, a.R);
+  return HISPARSE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t hisparse_pages_work_ints(int32_t num_pages, int32_t num_requests) {
+  if (num_pages < 1 || num_requests < 1 || num_pages > (1 << 30) || num_requests > 8192) return -1;
+  return kWorkHead + 3 * static_cast<int64_t>(std::max(num_pages, num_requests));
+}
+
+int hisparse_pages_grow(const hisparse_page_pool *p, const int32_t *d_reqs,
+                        const int32_t *d_blocks, int32_t n, void *stream) {
+  PoolArgs a;
+  if (const int rc = pool_args(p, a)) return rc;
+  if (n < 0 || (n > 0 && (!d_reqs || !d_blocks))) return HISPARSE_EINVAL;
+  if (n > a.R) return HISPARSE_EBOUND;
+  if (n == 0) return HISPARSE_OK;
+  a.n = n; a.src = d_reqs; a.want = d_blocks;
+  return launch_pdl(plan_kernel<false>, dim3(kPlanCtas), dim3(kPlanThreads), 0, stream, kPlanCtas, a);
+}
+
+int hisparse_pages_fork(const hisparse_page_pool *p, const int32_t *d_src, const int32_t *d_dst,
+                        const int32_t *d_tokens, int32_t n, void *stream) {
+  PoolArgs a;
+  if (const int rc = pool_args(p, a)) return rc;
+  if (n < 0 || (n > 0 && (!d_src || !d_dst || !d_tokens))) return HISPARSE_EINVAL;
+  if (n > a.R) return HISPARSE_EBOUND;
+  if (n == 0) return HISPARSE_OK;
+  a.n = n; a.src = d_src; a.dst = d_dst; a.want = d_tokens;
+  if (const int rc = launch_pdl(plan_kernel<true>, dim3(kPlanCtas), dim3(kPlanThreads), 0, stream,
+                                kPlanCtas, a))
+    return rc;
+  const int64_t items = static_cast<int64_t>(n) * a.layers;
+  return launch_pdl(page_copy_kernel<true>, dim3(static_cast<unsigned>(std::min<int64_t>(items, 456))),
+                    dim3(kCopyThreads), 0, stream, 1, a);
+}
+
+int hisparse_pages_free(const hisparse_page_pool *p, const int32_t *d_reqs, int32_t n,
+                        void *stream) {
+  PoolArgs a;
+  if (const int rc = pool_args(p, a)) return rc;
+  if (n < 0 || (n > 0 && !d_reqs)) return HISPARSE_EINVAL;
+  if (n == 0) return HISPARSE_OK;
+  a.n = n; a.src = d_reqs;
+  const int parts = std::min(8, (a.blocks + 255) / 256);
+  return launch_pdl(free_kernel, dim3(n, parts), dim3(256), 0, stream, 1, a);
+}
+
+int hisparse_pages_compact(const hisparse_page_pool *p, void *stream) {
+  PoolArgs a;
+  if (const int rc = pool_args(p, a)) return rc;
+  if (const int rc = launch_pdl(compact_plan_kernel, dim3(kPlanCtas), dim3(kPlanThreads), 0, stream,
+                                kPlanCtas, a))
+    return rc;
+  return launch_pdl(page_copy_kernel<false>, dim3(304), dim3(kCopyThreads), 0, stream, 1, a);
+}
+
+}  // extern "C"

@@ -11,12 +11,15 @@ import os
 from . import _build
 
 OK, EINVAL, EBOUND, ENOMEM, ECUDA, EROLE = 0, -1, -2, -3, -4, -5
-ERR_RANGE, ERR_DUP = 1, 2
+ERR_RANGE, ERR_DUP, ERR_FULL = 1, 2, 4
 RECORD_PLAN, SKIP_IO, FROM_MIRROR, UNION, WITH_SHARED = 1, 2, 4, 8, 16
 LOOKUP_PAGE_TABLE, LOOKUP_HASH = 0, 1
 HOST_HUGE, HOST_PINNED = 0, 1
+BF16, F16, F32 = 0, 1, 2
+ROTARY_INTERLEAVED, ROTARY_INVERSE = 1, 2
 
 _i32, _i64, _u32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_void_p
+_f32 = ctypes.c_float
 
 
 class Config(ctypes.Structure):
@@ -36,6 +39,55 @@ class Info(ctypes.Structure):
     _fields_ = [("ctas_per_request", _i32), ("threads_per_cta", _i32), ("smem_bytes", _i32),
                 ("hash_capacity", _i32), ("replay_ctas", _i32), ("sm_count", _i32),
                 ("metadata_bytes", _i64), ("lookup", _i32)]
+
+
+class RotaryTensor(ctypes.Structure):
+    _fields_ = [("x", _vp), ("y", _vp), ("x_token_stride", _i64), ("x_head_stride", _i64),
+                ("y_token_stride", _i64), ("y_head_stride", _i64), ("heads", _i32), ("dim", _i32)]
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("rot_dim", _i32), ("offset", _i32), ("flags", _u32),
+                ("tokens", _i64), ("amplitude", _f32), ("d_positions", _vp), ("d_turns", _vp),
+                ("t", RotaryTensor * 2)]
+
+
+class Records(ctypes.Structure):
+    _fields_ = [("kv_heads", _i32), ("k_dim", _i32), ("v_dim", _i32), ("latent", _i32),
+                ("block_tokens", _i32)]
+
+
+class PackArgs(ctypes.Structure):
+    _fields_ = [("rec", Records), ("dtype", _i32), ("n", _i32), ("max_len", _i32),
+                ("num_requests", _i32), ("scale_blocks", _i32), ("headroom", _f32),
+                ("d_cu_lens", _vp), ("d_start", _vp), ("d_reqs", _vp), ("tokens", _i64),
+                ("k", _vp), ("v", _vp), ("k_token_stride", _i64), ("k_head_stride", _i64),
+                ("v_token_stride", _i64), ("v_head_stride", _i64), ("scales", _vp),
+                ("scales_req_stride", _i64), ("dst", _vp), ("dst_rows", _i64),
+                ("dst_row_stride", _i64), ("dst_req_stride", _i64), ("d_blocks", _vp),
+                ("max_blocks", _i32), ("page_tokens", _i32), ("rot_dim", _i32),
+                ("rot_offset", _i32), ("rot_flags", _u32), ("amplitude", _f32), ("d_turns", _vp),
+                ("d_status", _vp)]
+
+
+class AttendArgs(ctypes.Structure):
+    _fields_ = [("rec", Records), ("dtype", _i32), ("num_requests", _i32), ("rows", _i32),
+                ("entries", _i32), ("heads", _i32), ("buffer_slots", _i32),
+                ("record_tokens", _i32), ("sel_block_tokens", _i32), ("softmax_scale", _f32),
+                ("q", _vp), ("q_row_stride", _i64), ("q_head_stride", _i64), ("out", _vp),
+                ("out_row_stride", _i64), ("out_head_stride", _i64), ("lse", _vp),
+                ("d_sel", _vp), ("d_slots", _vp), ("hot", _vp), ("hot_req_stride", _i64),
+                ("hot_row_stride", _i64), ("resident", _vp), ("resident_rows", _i64),
+                ("resident_row_stride", _i64), ("scales", _vp), ("scales_req_stride", _i64),
+                ("scale_blocks", _i32), ("d_seq_lens", _vp), ("d_num_reqs", _vp),
+                ("d_status", _vp)]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [("num_pages", _i32), ("num_requests", _i32), ("max_blocks", _i32),
+                ("page_tokens", _i32), ("layers", _i32), ("row_bytes", _i64), ("store", _vp),
+                ("layer_stride", _i64), ("page_stride", _i64), ("d_tables", _vp),
+                ("d_refs", _vp), ("d_work", _vp), ("d_status", _vp)]
 
 
 # (name, restype, argtypes) of every exported symbol, in header order
@@ -59,6 +111,14 @@ SIGNATURES = [
     ("hisparse_export_plan", _i32, [_vp, _i32, _vp, _vp, _vp]),
     ("hisparse_reset", _i32, [_vp, _i32, _vp]),
     ("hisparse_set_l2_persisting", _i32, [_vp, _i64]),
+    ("hisparse_rotary", _i32, [ctypes.POINTER(RotaryArgs), _vp]),
+    ("hisparse_pack", _i32, [ctypes.POINTER(PackArgs), _vp]),
+    ("hisparse_attend", _i32, [ctypes.POINTER(AttendArgs), _vp]),
+    ("hisparse_pages_work_ints", _i64, [_i32, _i32]),
+    ("hisparse_pages_grow", _i32, [ctypes.POINTER(PagePool), _vp, _vp, _i32, _vp]),
+    ("hisparse_pages_fork", _i32, [ctypes.POINTER(PagePool), _vp, _vp, _vp, _i32, _vp]),
+    ("hisparse_pages_free", _i32, [ctypes.POINTER(PagePool), _vp, _i32, _vp]),
+    ("hisparse_pages_compact", _i32, [ctypes.POINTER(PagePool), _vp]),
     ("hisparse_get_info", _i32, [_vp, ctypes.POINTER(Info)]),
     ("hisparse_host_alloc", _i32, [ctypes.c_size_t, ctypes.POINTER(_vp)]),
     ("hisparse_host_free", _i32, [_vp]),
@@ -221,3 +281,36 @@ def hisparse_host_hugepage_bytes(p, nbytes):
 
 def hisparse_admit(h, layer, d_reqs, n, d_preload, stream):
     return load().hisparse_admit(h, layer, d_reqs, n, d_preload, stream)
+
+
+# ---- 8-bit records and resident pages --------------------------------------
+def hisparse_rotary(args, stream):
+    return load().hisparse_rotary(args, stream)
+
+
+def hisparse_pack(args, stream):
+    return load().hisparse_pack(args, stream)
+
+
+def hisparse_attend(args, stream):
+    return load().hisparse_attend(args, stream)
+
+
+def hisparse_pages_work_ints(num_pages, num_requests):
+    return load().hisparse_pages_work_ints(num_pages, num_requests)
+
+
+def hisparse_pages_grow(pool, d_reqs, d_blocks, n, stream):
+    return load().hisparse_pages_grow(pool, d_reqs, d_blocks, n, stream)
+
+
+def hisparse_pages_fork(pool, d_src, d_dst, d_tokens, n, stream):
+    return load().hisparse_pages_fork(pool, d_src, d_dst, d_tokens, n, stream)
+
+
+def hisparse_pages_free(pool, d_reqs, n, stream):
+    return load().hisparse_pages_free(pool, d_reqs, n, stream)
+
+
+def hisparse_pages_compact(pool, stream):
+    return load().hisparse_pages_compact(pool, stream)

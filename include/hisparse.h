@@ -58,6 +58,7 @@ extern "C" {
 #define HISPARSE_ERR_RANGE 1u /* a selected position outside [-1, P), or a
                                  newest / write-back position outside [-1, P) */
 #define HISPARSE_ERR_DUP 2u   /* one position selected twice by one request */
+#define HISPARSE_ERR_FULL 4u  /* too few free pages (hisparse_pages_*) */
 
 /* ---- resolve flags ----------------------------------------------------- */
 #define HISPARSE_RECORD_PLAN 1u /* record the miss plan for shared layers ([DD] §5.5) */
@@ -461,6 +462,221 @@ int hisparse_host_alloc_kind(size_t bytes, int32_t kind, void **out);
  * costs the GPU more address-translation work per fetched record.
  * Errors: EINVAL. */
 int hisparse_host_hugepage_bytes(const void *p, size_t bytes, size_t *huge_out);
+
+/* ======================================================================== */
+/* 8-bit records: rotary positions, packing, attention, resident pages.      */
+/*                                                                           */
+/* (Library calls, not steps of the pages' method: the work on either side   */
+/* of RESOLVE in a decode layer.)  hisparse_rotary turns q and k,            */
+/* hisparse_pack makes the records that the host pool, the resident store    */
+/* and d_new_rows hold, hisparse_attend reads the rows that RESOLVE's slot   */
+/* vector names, and hisparse_pages_* keep the block tables and pages of the */
+/* resident tier (d_res_blocks).  None of them needs a handle.  They launch  */
+/* asynchronously on `stream`, never allocate, never synchronise, and can be */
+/* captured in a graph.  Errors in device-side inputs set HISPARSE_ERR_*     */
+/* bits in *d_status (a caller's uint32, may be NULL); nothing out of range  */
+/* is read or written.                                                       */
+/* ======================================================================== */
+
+/* element types of tensors */
+#define HISPARSE_BF16 0
+#define HISPARSE_F16 1
+#define HISPARSE_F32 2
+
+/* hisparse_rotary flags */
+#define HISPARSE_ROTARY_INTERLEAVED 1u /* pairs (2i, 2i+1); else (i, i + rot_dim/2) */
+#define HISPARSE_ROTARY_INVERSE 2u     /* turn by the negative angle: the gradient of the
+                                          rotation, and its inverse at amplitude 1 */
+
+/* One tensor [tokens][heads][dim] to rotate.  Strides are in elements; the
+ * last dimension is contiguous.  x == y rotates in place; otherwise the two do
+ * not overlap, and the values outside the rotated part are copied. */
+typedef struct {
+  const void *x;
+  void *y;
+  int64_t x_token_stride, x_head_stride;
+  int64_t y_token_stride, y_head_stride;
+  int32_t heads; /* 0: no tensor */
+  int32_t dim;
+} hisparse_rotary_tensor;
+
+typedef struct {
+  int32_t dtype;   /* HISPARSE_BF16, _F16 or _F32, of every tensor */
+  int32_t rot_dim; /* even; values [offset, offset + rot_dim) of each head turn */
+  int32_t offset;
+  uint32_t flags;
+  int64_t tokens;
+  float amplitude;            /* both results of a pair are multiplied by it */
+  const int32_t *d_positions; /* [tokens] */
+  const int64_t *d_turns;     /* [rot_dim / 2] turns per position of pair i as a 64-bit binary
+                                 fraction: round(f_i / 2pi * 2^64) mod 2^64, f_i in radians per
+                                 position.  position * turns mod 2^64 is the phase, exact at
+                                 every position. */
+  hisparse_rotary_tensor t[2]; /* q and k, say */
+} hisparse_rotary_args;
+
+/* Rotary positions: pair (a, b) of token t becomes amplitude * (a cos - b sin,
+ * a sin + b cos) at the angle 2pi * frac(d_positions[t] * turns).  Computed in
+ * 32 bits and rounded once.  Any strides and alignments of whole elements.
+ * Errors: EINVAL (NULL, rot_dim odd or < 2, a rotated part outside the head,
+ * unknown type), ECUDA. */
+int hisparse_rotary(const hisparse_rotary_args *args, void *stream);
+
+/* What a record of e4m3 bytes holds.  A token's row is kv_heads K heads of
+ * k_dim bytes, then kv_heads V heads of v_dim bytes; with latent = 1 there is
+ * no V part and the first v_dim values of a K head are V as well (v_dim <=
+ * k_dim).  The value of a byte is e4m3(byte) * scale, one float32 scale for each
+ * block of block_tokens positions and head: scales[request][block][c], c =
+ * K heads, then V heads (K heads only when latent).  k_dim and v_dim are
+ * multiples of 16; k_dim <= 640, v_dim <= 512, block_tokens <= 4096. */
+typedef struct {
+  int32_t kv_heads, k_dim, v_dim, latent, block_tokens;
+} hisparse_records;
+
+typedef struct {
+  hisparse_records rec;
+  int32_t dtype;    /* of k and v */
+  int32_t n;        /* sequences in the call */
+  int32_t max_len;  /* at least the longest sequence's tokens in the call, >= 1 */
+  int32_t num_requests; /* R of the scale table (and of the rows, by position or page) */
+  int32_t scale_blocks; /* blocks of a request in the scale table */
+  float headroom;   /* >= 1; see below */
+  const int32_t *d_cu_lens; /* [n + 1] tokens of sequence i are cu[i] .. cu[i+1]-1 of k and v;
+                               NULL: max_len tokens each */
+  const int32_t *d_start;   /* [n] position of each sequence's first token of the call */
+  const int32_t *d_reqs;    /* [n] request of each sequence, distinct; NULL: i */
+  int64_t tokens;           /* rows of k and v */
+  const void *k, *v;        /* [tokens][kv_heads][k_dim], ..[v_dim] (v NULL when latent) */
+  int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride; /* elements */
+  float *scales;            /* [num_requests][scale_blocks][columns], updated */
+  int64_t scales_req_stride; /* floats */
+  /* where the rows go: exactly one of three */
+  void *dst;
+  int64_t dst_rows;         /* rows that dst holds (per request, by position) */
+  int64_t dst_row_stride;   /* bytes, multiple of 16 */
+  int64_t dst_req_stride;   /* bytes; != 0: by position, row p of request r; else by token t of
+                               the call, or by page: */
+  const int32_t *d_blocks;  /* [num_requests][max_blocks] page table: position p is row
+                               d_blocks[r][p / page_tokens] * page_tokens + p % page_tokens;
+                               tokens without a page are not stored */
+  int32_t max_blocks, page_tokens;
+  /* K turned on the way (rot_dim 0: not); rot_dim a multiple of 16, offset of 8 */
+  int32_t rot_dim, rot_offset;
+  uint32_t rot_flags;
+  float amplitude;
+  const int64_t *d_turns;
+  uint32_t *d_status;
+} hisparse_pack_args;
+
+/* Pack K and V of new tokens into records.  The scale of a (block, head):
+ * - the call holds the block's first position, or the block's scale is 0 (unset):
+ *   amax / 448 over the call's tokens of the block, times `headroom` unless the
+ *   call also holds the block's last position (amax 0 leaves it 0, not set);
+ * - else the block is open and its scale stands.
+ * A value x is stored as e4m3(x / scale), rounded to nearest even, saturating
+ * at 448; infinities do not count in amax and saturate; NaN stays NaN.  A decode step's
+ * rows are d_new_rows of hisparse_resolve_step; a prompt's go to the host pool,
+ * a mirror or the resident store.  Start the scales of a new request at 0.
+ * A position outside [0, scale_blocks * block_tokens), a request outside
+ * [0, R), or a row outside dst sets HISPARSE_ERR_RANGE; its token is skipped.
+ * Errors: EINVAL, EBOUND (sizes of hisparse_records), ECUDA. */
+int hisparse_pack(const hisparse_pack_args *args, void *stream);
+
+typedef struct {
+  hisparse_records rec;
+  int32_t dtype;        /* of q and out: HISPARSE_BF16 or HISPARSE_F16 */
+  int32_t num_requests; /* R */
+  int32_t rows;         /* query rows per request (verify rows), >= 1 */
+  int32_t entries;      /* selected records per query row: top_k = rows * entries */
+  int32_t heads;        /* query heads, a multiple of kv_heads; head h reads KV head
+                           h / (heads / kv_heads) */
+  int32_t buffer_slots; /* B: slots 0..B of the hot buffer, row B the newest */
+  int32_t record_tokens; /* tokens of a record (a page), >= 1 */
+  int32_t sel_block_tokens; /* > 1: d_sel holds block ids, as hisparse_resolve_options */
+  float softmax_scale;
+  const void *q;        /* [R][rows][heads][k_dim] */
+  int64_t q_row_stride, q_head_stride;     /* elements, multiples of 8 */
+  void *out;            /* [R][rows][heads][v_dim] */
+  int64_t out_row_stride, out_head_stride; /* elements, multiples of 8 */
+  float *lse;           /* [R][rows][heads] log of the softmax sum, or NULL */
+  const int32_t *d_sel;   /* [R][rows * entries] selected records (RESOLVE's input) */
+  const int32_t *d_slots; /* [R][rows * entries] their rows (RESOLVE's output) */
+  const void *hot;        /* [R][B + 1] records */
+  int64_t hot_req_stride, hot_row_stride; /* bytes, multiples of 16 */
+  const void *resident;   /* rows of slots above B (slot - B - 1), or NULL */
+  int64_t resident_rows, resident_row_stride;
+  const float *scales;    /* [R][scale_blocks][columns] */
+  int64_t scales_req_stride; /* floats */
+  int32_t scale_blocks;
+  const int32_t *d_seq_lens; /* [R] positions of each request, or NULL: tokens at or beyond it
+                                (a part-filled last page) do not count */
+  const int32_t *d_num_reqs; /* device int32, or NULL: requests at or beyond it are untouched */
+  uint32_t *d_status;
+} hisparse_attend_args;
+
+/* Sparse attention over records: for query row i of request r and head h, over
+ * its entries j with slot >= 0 and the tokens of their records,
+ *   s_j = softmax_scale * q . (k_j * sK),  out = sum_j softmax(s)_j (v_j * sV),
+ * lse = log sum_j exp(s_j).  A row with nothing to read gives out 0 and lse
+ * -inf.  Scores, softmax and sums are in 32 bits; K and V enter the tensor
+ * cores as the e4m3 they are, q and the probabilities as sums of e4m3 terms
+ * (two for bf16, three for f16) at least as fine as their type.  A slot
+ * outside what B, resident and -1 allow, or a selected position outside
+ * the scale table, sets HISPARSE_ERR_RANGE and is left out.
+ * Errors: EINVAL, EBOUND (sizes of hisparse_records), ECUDA. */
+int hisparse_attend(const hisparse_attend_args *args, void *stream);
+
+/* The pages of the resident tier: a store of num_pages pages of page_tokens
+ * rows in each of `layers` layers, one block table for all layers (d_res_blocks
+ * of hisparse_resolve_resident), and a count of the table entries that name
+ * each page.  The caller owns all of it: counts start at 0 and tables at -1.
+ * Calls on one pool are ordered by the caller (one stream, or events).  Free pages
+ * are those with count 0; new pages are always the lowest free ones, in the
+ * order of the call's list, so results do not depend on timing. */
+typedef struct {
+  int32_t num_pages, num_requests, max_blocks, page_tokens, layers;
+  int64_t row_bytes;     /* multiple of 16 */
+  void *store;           /* row t of page p of layer l: store + l*layer_stride +
+                            p*page_stride + t*row_bytes */
+  int64_t layer_stride, page_stride; /* bytes, multiples of 16 */
+  int32_t *d_tables;     /* [num_requests][max_blocks], page or -1 */
+  int32_t *d_refs;       /* [num_pages] */
+  int32_t *d_work;       /* hisparse_pages_work_ints int32, contents of no meaning
+                            between calls */
+  uint32_t *d_status;
+} hisparse_page_pool;
+
+/* int32 words of d_work for a pool of these sizes (-1: bad sizes). */
+int64_t hisparse_pages_work_ints(int32_t num_pages, int32_t num_requests);
+
+/* Give request d_reqs[i] pages for its blocks 0 .. d_blocks[i]-1 that have
+ * none.  A request whose turn finds too few free pages after those
+ * that come before it in the list gets none (HISPARSE_ERR_FULL), nor does any later one.  n <=
+ * num_requests, requests distinct.  Errors: EINVAL, EBOUND, ECUDA. */
+int hisparse_pages_grow(const hisparse_page_pool *p, const int32_t *d_reqs,
+                        const int32_t *d_blocks, int32_t n, void *stream);
+
+/* Request d_dst[i], which holds no page, becomes a copy of the first
+ * d_tokens[i] positions of request d_src[i]: whole blocks are shared (their
+ * counts grow), and the rows in use of a part-filled last block are copied in
+ * every layer to a new page, so that both can go on writing.  Blocks the
+ * source has no page for stay without one.  Destinations are distinct and are
+ * not sources of the same call; n <= num_requests.  A destination that holds
+ * pages, or an index or length out of range, is skipped with
+ * HISPARSE_ERR_RANGE; too few free pages as hisparse_pages_grow.
+ * Errors: EINVAL, EBOUND, ECUDA. */
+int hisparse_pages_fork(const hisparse_page_pool *p, const int32_t *d_src, const int32_t *d_dst,
+                        const int32_t *d_tokens, int32_t n, void *stream);
+
+/* Release every page of the listed requests: their table rows become -1 and
+ * the counts fall.  Errors: EINVAL, ECUDA. */
+int hisparse_pages_free(const hisparse_page_pool *p, const int32_t *d_reqs, int32_t n,
+                        void *stream);
+
+/* Move the pages in use to the front of the store: with m pages in use, the
+ * j-th of those at or above m moves to the j-th free page below m, in every
+ * layer, and every table follows.  No other page moves.  Errors: EINVAL, ECUDA. */
+int hisparse_pages_compact(const hisparse_page_pool *p, void *stream);
 
 /* (Library calls.)
  * The cudaError_t of the last failed CUDA call made by this thread through
