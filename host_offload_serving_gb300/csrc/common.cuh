@@ -74,7 +74,7 @@ __device__ __forceinline__ void pdl_launch() {
 struct FastDiv {
   uint32_t d, mul, shift;
   FastDiv() = default;
-  explicit FastDiv(uint32_t div) : d(div) {
+  __host__ __device__ explicit FastDiv(uint32_t div) : d(div) {
     shift = 0;
     while ((1ull << shift) < div) ++shift;
     mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - div)) / div + 1);

@@ -59,6 +59,8 @@ extern "C" {
                                  newest / write-back position outside [-1, P) */
 #define HISPARSE_ERR_DUP 2u   /* one position selected twice by one request */
 #define HISPARSE_ERR_FULL 4u  /* too few free pages (hisparse_pages_*) */
+#define HISPARSE_ERR_WAIT 8u  /* a kernel gave up a wait on its own work; results of that
+                                 launch are not to be used */
 
 /* ---- resolve flags ----------------------------------------------------- */
 #define HISPARSE_RECORD_PLAN 1u /* record the miss plan for shared layers ([DD] §5.5) */
