@@ -18,9 +18,9 @@
 // (p_j sV_j is what multiplies the raw bytes of V), through the exponent, so the
 // running maximum is over s_j + log2(sV_j) and no product leaves the range.
 //
-// Warps: 0-3 softmax (a lane a token, TMEM lane = token), 4-7 gather (16-byte cp.async
-// into the 128-byte-swizzled tiles the tensor cores read, several tiles ahead),
-// 8 issues the products.  S is double buffered in TMEM, so the scores of tile i+1
+// Warps: four softmax warps (a lane a token, TMEM lane = token) for each 32 columns, four that
+// gather (16-byte cp.async into the 128-byte-swizzled tiles the tensor cores read,
+// several tiles ahead), and one that issues the products.  S is double buffered in TMEM, so the scores of tile i+1
 // are computed while the softmax of tile i runs.  O is rescaled only where a column's
 // maximum has grown by more than 2^2.75 since it was last set.
 #include <algorithm>
@@ -30,8 +30,7 @@
 
 namespace {
 
-constexpr int kSoft = 4, kGather = 4;
-constexpr int kThreads = 32 * (kSoft + kGather + 1);
+constexpr int kGather = 4;  // warps that gather
 constexpr int kMaxStages = 6;
 constexpr int kMaxCluster = 16;
 constexpr float kTop = 6.f;     // log2 of a column's largest probability when its offset is set
@@ -60,7 +59,7 @@ struct AttendArgs {
   int64_t row_bytes;  // a token's part of a record
   // the launch's plan
   int32_t cluster, per_cta, tile, stages, k_chunks, v_chunks, v_tiles, tmem_cols;
-  FastDiv by_row;
+  FastDiv quads;  // v_dim / 4
   uint32_t stage_bytes, off_q, off_p, off_meta, off_misc;
 };
 
@@ -73,6 +72,17 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 }
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {  // never suspends
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -111,27 +121,38 @@ __device__ __forceinline__ void tc_before() {
 __device__ __forceinline__ void tc_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r)::"memory");
+  return r;
+}
+// The elected lane's mbarrier arrival once its products so far are done.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t elected) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+      "r"(elected)
+      : "memory");
 }
 // Shared-memory descriptor of a 128-byte-swizzled operand whose groups of 8 rows are 1024
-// bytes apart (either major-ness: the other offset is not used).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
-         (2ull << 61);
-}
+// bytes apart (either major-ness: the other offset is not used).  Its lower word; the
+// upper one is the same for all.
+constexpr uint32_t kDescHi = 64u | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t smem_desc(uint32_t addr) { return addr >> 4 | 1u << 16; }
 // Instruction descriptor: f32 accumulator, A e4m3, B e4m3 or e5m2, M = 128.
 __device__ __forceinline__ uint32_t mma_desc(int n, bool b_e5m2, bool transposed) {
   return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (transposed ? 3u << 15 : 0u) |
          (static_cast<uint32_t>(n) >> 3 << 17) | (128u >> 4 << 24);
 }
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       uint32_t accumulate) {
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t elected) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, e;\n .reg .b64 da, db;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " mov.b64 da, {%1, %6};\n mov.b64 db, {%2, %6};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(elected), "r"(kDescHi)
       : "memory");
 }
 #define TC_REGS16(r)                                                                        \
@@ -193,17 +214,20 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ bool soft_any(bool x) {  // OR over the softmax warps, and their barrier
+// OR over a group of four softmax warps, and their barrier.
+__device__ __forceinline__ bool soft_any(int group, bool x) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n"
-      " barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+      " barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x))
+      : "r"(static_cast<uint32_t>(x)), "r"(group + 1)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void soft_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void soft_sync(int group) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(group + 1) : "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
@@ -287,19 +311,31 @@ __device__ __forceinline__ void column_sums(float (&l)[N], int lane) {
   if constexpr (O > 1) column_sums<N, O / 2, kHalf / 2>(l, lane);
 }
 
+template <int N>
+struct Shape {
+  static constexpr int groups = N > 32 ? N / 32 : 1;  // of four softmax warps
+  static constexpr int cols = N / groups;             // columns of a softmax thread
+  static constexpr int soft = 4 * groups;             // softmax warps
+  static constexpr int workers = soft + kGather;
+  static constexpr int threads = 32 * (workers + 1);
+};
+
 template <class T, int N>
-__global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_kernel(const AttendArgs a) {
   constexpr int kTerms = Terms<T>::n;
+  constexpr int NC = Shape<N>::cols, kSoft = Shape<N>::soft, kWorkers = Shape<N>::workers;
+  constexpr int kThreads = Shape<N>::threads;
   extern __shared__ char smem_raw[];
   __shared__ uint64_t s_bars[2 * kMaxStages + 5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
-  __shared__ float s_m[N], s_l[N], s_f[N], s_qf[N], s_wmax[kSoft][N], s_w[kMaxCluster * N];
+  __shared__ float s_m[N], s_l[N], s_f[N], s_wmax[4][N], s_w[kMaxCluster * N];
+  __shared__ __align__(16) float s_qf[N];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = smem_u32(s_bars);
   const uint32_t b_full = bars, b_empty = bars + 8 * kMaxStages, b_s = bars + 16 * kMaxStages;
   const uint32_t b_p = b_s + 16, b_pv = b_s + 24, b_q = b_s + 32;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = a.cluster > 1 ? blockIdx.x % a.cluster : 0;
   const uint32_t unit = blockIdx.x / a.cluster;
   const uint32_t hg = unit % a.hgroups, kvh = unit / a.hgroups % a.kv_heads;
@@ -307,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
   const int req = static_cast<int>(qrow / a.rows);
 
   if (tid == 0) {
-    for (int s = 0; s < kMaxStages; ++s) {
+    for (int s = 0; s < a.stages; ++s) {
       bar_init(b_full + 8 * s, 32 * kGather);
       bar_init(b_empty + 8 * s, 1);
     }
@@ -315,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
     bar_init(b_s + 8, 1);
     bar_init(b_p, 32 * kSoft);
     bar_init(b_pv, 1);
-    bar_init(b_q, 32 * (kSoft + kGather));
+    bar_init(b_q, 32 * kWorkers);
     s_fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -332,11 +368,11 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
       const int n = i % N, term = i / N;
       st_shared4(base + a.off_q + ((term * a.k_chunks + c) * N + n) * 128 + ((j ^ (n & 7)) << 4), 0, 0, 0, 0);
     }
+    fence_async();
   }
-  fence_async();
   pdl_wait();
   if (a.num_reqs && req >= *a.num_reqs) return;  // the whole cluster
-  if (warp == kSoft + kGather) {
+  if (warp == kWorkers) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                  "r"(a.tmem_cols)
                  : "memory");
@@ -355,25 +391,27 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
   const int64_t entry0 = qrow * a.entries;
   volatile int *fail = &s_fail;
 
-  // Query heads of this group into e4m3 terms, a warp a head in turn of 8 warps.
+  // Query heads of this group into e4m3 terms, a warp a head in turn of the workers.
   auto make_q = [&](int w) {
     const int vecs = a.k_dim >> 3;
     const T *q0 = static_cast<const T *>(a.q) + qrow * a.q_row;
-    constexpr int kBatch = N / 8 < 4 ? N / 8 : 4;
+    constexpr int kTurns = (N + kWorkers - 1) / kWorkers;
+    constexpr int kBatch = kTurns < 3 ? kTurns : kTurns == 4 ? 4 : 3;
 #pragma unroll 1
-    for (int n0 = w; n0 < N; n0 += 8 * kBatch) {
+    for (int n0 = w; n0 < N; n0 += kWorkers * kBatch) {
       uint4 v[kBatch][3];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int h = static_cast<int>(hg) * N + n0 + 8 * b;
+        const int n = n0 + kWorkers * b, h = static_cast<int>(hg) * N + n;
         const uint4 *src = reinterpret_cast<const uint4 *>(q0 + static_cast<int64_t>(kvh * a.group + h) * a.q_head);
 #pragma unroll
         for (int i = 0; i < 3; ++i)
-          v[b][i] = h < a.group && lane + 32 * i < vecs ? src[lane + 32 * i] : make_uint4(0, 0, 0, 0);
+          v[b][i] = n < N && h < a.group && lane + 32 * i < vecs ? src[lane + 32 * i] : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int n = n0 + 8 * b;
+        const int n = n0 + kWorkers * b;
+        if (n >= N) break;
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
@@ -391,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
                                  : NAN;
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
+          if (32 * i >= vecs) break;
           if (lane + 32 * i >= vecs) continue;
           const T *e = reinterpret_cast<const T *>(&v[b][i]);
           float x[8];
@@ -419,22 +458,16 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
     // ---- softmax ---------------------------------------------------------------
     make_q(warp);
     bar_wait(b_q, 0, fail);  // the factors of all heads
-    float l[N];
+    const int grp = warp >> 2, wl = warp & 3, c0 = grp * NC, gt = tid & 127;
+    float l[NC];
 #pragma unroll
-    for (int c = 0; c < N; ++c) l[c] = 0.f;
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const int tk = warp * 32 + lane;
+    for (int c = 0; c < NC; ++c) l[c] = 0.f;
+    const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
+    const int tk = wl * 32 + lane;
     const uint32_t p_row = base + a.off_p + tk * 128;
     for (int i = 0; i < tiles; ++i) {
       const int s = i % a.stages, cn = min(a.tile, t1 - t0 - i * a.tile);
       bar_wait(b_full + 8 * s, (i / a.stages) & 1, fail);
-      bar_wait(b_s + 8 * (i & 1), (i >> 1) & 1, fail);
-      __syncwarp();
-      tc_after();
-      float x[N];
-#pragma unroll
-      for (int c = 0; c < N; c += 16)
-        tc_ld16(tmem + lanes + (i & 1) * N + c, reinterpret_cast<uint32_t *>(x + c));
       float ks = 0.f, lv = 0.f, iv = 1.f;
       bool use = false;
       if (tk < cn) {
@@ -451,32 +484,39 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
           iv = 1.f / v;
         }
       }
+      bar_wait(b_s + 8 * (i & 1), (i >> 1) & 1, fail);
+      __syncwarp();
+      tc_after();
+      float x[NC];
 #pragma unroll
-      for (int c = 0; c < N; c += 16) tc_wait_ld16(reinterpret_cast<uint32_t *>(x + c));
+      for (int c = 0; c < NC; c += 16)
+        tc_ld16(tmem + lanes + (i & 1) * N + c0 + c, reinterpret_cast<uint32_t *>(x + c));
+#pragma unroll
+      for (int c = 0; c < NC; c += 16) tc_wait_ld16(reinterpret_cast<uint32_t *>(x + c));
       // scores in powers of two, the V scale in them
-      float mine = -INFINITY, mine2 = -INFINITY;  // lane c keeps the maxima of columns c, c + 32
+      float mine = -INFINITY;  // lane c keeps the maximum of column c
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
-        x[c] = use ? fmaf(x[c] * ks, s_qf[c], lv) : -INFINITY;
+      for (int c = 0; c < NC; ++c) {
+        x[c] = use ? fmaf(x[c] * ks, s_qf[c0 + c], lv) : -INFINITY;
         const float m = warp_max(x[c]);
-        if (lane == (c & 31)) (c < 32 ? mine : mine2) = m;
+        if (lane == c) mine = m;
       }
-      if (lane < N) s_wmax[warp][lane] = mine;
-      if (N > 32) s_wmax[warp][lane + 32 < N ? lane + 32 : 0] = N > 32 ? mine2 : mine;
-      soft_sync();
+      if (lane < NC) s_wmax[wl][c0 + lane] = mine;
+      soft_sync(grp);
       bool moved = false;
-      if (tid < N) {
-        const float m = fmaxf(fmaxf(s_wmax[0][tid], s_wmax[1][tid]), fmaxf(s_wmax[2][tid], s_wmax[3][tid]));
-        const float old = s_m[tid];
+      if (gt < NC) {
+        const int c = c0 + gt;
+        const float m = fmaxf(fmaxf(s_wmax[0][c], s_wmax[1][c]), fmaxf(s_wmax[2][c], s_wmax[3][c]));
+        const float old = s_m[c];
         float f = 1.f;
         if (m > -INFINITY && !(m - old <= kSlack)) {
           f = old > -INFINITY ? ex2(old - (m - kTop)) : 0.f;
-          s_m[tid] = m - kTop;
+          s_m[c] = m - kTop;
           moved = true;
         }
-        s_f[tid] = f;
+        s_f[c] = f;
       }
-      moved = soft_any(moved);
+      moved = soft_any(grp, moved);
       if (i > 0) {
         bar_wait(b_pv, (i - 1) & 1, fail);  // O and the probabilities' buffer are free
         __syncwarp();
@@ -484,25 +524,25 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
       }
       if (moved) {
 #pragma unroll
-        for (int c = 0; c < N; ++c) l[c] *= s_f[c];
+        for (int c = 0; c < NC; ++c) l[c] *= s_f[c0 + c];
         if (i > 0) {
           for (int j = 0; j < a.v_tiles; ++j)
 #pragma unroll
-            for (int c = 0; c < N; c += 16) {
+            for (int c = 0; c < NC; c += 16) {
               uint32_t o[16];
-              const uint32_t at = t_o + lanes + j * N + c;
+              const uint32_t at = t_o + lanes + j * N + c0 + c;
               tc_ld16(at, o);
               tc_wait_ld16(o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_f[c + e]);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_f[c0 + c + e]);
               tc_st16(at, o);
             }
           tc_wait_st();
         }
       }
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
-        const float m = s_m[c];
+      for (int c = 0; c < NC; ++c) {
+        const float m = s_m[c0 + c];
         x[c] = ex2(x[c] - (m > -INFINITY ? m : 0.f));
         l[c] = fmaf(x[c], iv, l[c]);
       }
@@ -510,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
 #pragma unroll
         for (int t = 0; t < kTerms; ++t)
 #pragma unroll
-          for (int c = 0; c < N; c += 16) {
+          for (int c = 0; c < NC; c += 16) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -523,37 +563,39 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
                 w[e] |= take_term<true>(y[2], y[3]) << 16;
               }
             }
-            st_shared4(p_row + (((t * N + c) >> 4 ^ (tk & 7)) << 4), w[0], w[1], w[2], w[3]);
+            st_shared4(p_row + (((t * N + c0 + c) >> 4 ^ (tk & 7)) << 4), w[0], w[1], w[2], w[3]);
           }
       }
       fence_async();
       tc_before();
       bar_arrive(b_p);
     }
+    column_sums<NC, 16, NC / 2>(l, lane);
+    soft_sync(grp);  // s_wmax is free
+    if (NC == 32) {
+      s_wmax[wl][c0 + lane] = l[0];
+    } else if ((lane & 1) == 0) {
+      s_wmax[wl][c0 + (lane >> 1)] = l[0];
+    }
+    soft_sync(grp);
+    if (gt < NC) {
+      const int c = c0 + gt;
+      const float z = (s_wmax[0][c] + s_wmax[1][c]) + (s_wmax[2][c] + s_wmax[3][c]);
+      s_l[c] = z;
+      s_f[c] = z > 0.f || z != z ? 1.f / z : 0.f;
+    }
     if (tiles > 0) {
       bar_wait(b_pv, (tiles - 1) & 1, fail);
       tc_after();
     }
     __syncwarp();
-    column_sums<N, 16, N / 2>(l, lane);
-    soft_sync();  // s_wmax is free
-    if constexpr (N == 64) {
-      s_wmax[warp][2 * lane] = l[0];
-      s_wmax[warp][2 * lane + 1] = l[1];
-    } else if (N == 32) {
-      s_wmax[warp][lane] = l[0];
-    } else if ((lane & 1) == 0) {
-      s_wmax[warp][lane >> 1] = l[0];
-    }
-    soft_sync();
-    if (tid < N) s_l[tid] = (s_wmax[0][tid] + s_wmax[1][tid]) + (s_wmax[2][tid] + s_wmax[3][tid]);
-  } else if (warp < kSoft + kGather) {
+  } else if (warp < kWorkers) {
     // ---- gather ------------------------------------------------------------------
     const int pw = warp - kSoft, per = a.tile / kGather;
-    const int kc = a.k_dim >> 4, vc = a.latent ? 0 : a.v_dim >> 4, cpr = kc + vc;
-    const FastDiv by_row = a.by_row;
+    const int kc = a.k_dim >> 4, cpr = kc + (a.latent ? 0 : a.v_dim >> 4);
     const int64_t k_at = static_cast<int64_t>(kvh) * a.k_dim;
-    const int64_t v_at = static_cast<int64_t>(a.kv_heads) * a.k_dim + static_cast<int64_t>(kvh) * a.v_dim - 16 * kc;
+    // from a K head's first byte to where its V head would begin 16 * kc bytes earlier
+    const int64_t v_at = static_cast<int64_t>(a.kv_heads) * a.k_dim + static_cast<int64_t>(kvh) * a.v_dim - 16 * kc - k_at;
     const int seq = a.seq_lens ? a.seq_lens[req] : INT32_MAX;
     const float *scales = a.scales + req * a.scales_req + kvh;
     const char *hot = a.hot + req * a.hot_req;
@@ -600,33 +642,38 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
     int issued = 0, signalled = 0;
     Token cur = token(raw(0), 0);
     Raw next = raw(1);
+    // A tile's rows, `per` of them this warp's: 16-byte chunks in passes of a power of two of
+    // columns, so that a lane's column, and with it all but the row, is fixed in a pass.
     auto issue = [&]() {
       const int i = issued, s = i % a.stages;
       const int cn = min(a.tile, t1 - t0 - i * a.tile);
       const Token ahead = token(next, i + 1);
       next = raw(i + 2);
-      const uint32_t st = base + s * a.stage_bytes;
       if (lane < per)
         asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(base + a.off_meta + (s * a.tile + pw * per + lane) * 8),
                      "f"(cur.row ? cur.k : __int_as_float(0x7fffffff)), "f"(cur.v)
                      : "memory");
-      const uint64_t row = reinterpret_cast<uint64_t>(cur.row);
+      const uint32_t have = __ballot_sync(0xffffffffu, cur.row != nullptr);
+      const uint64_t row = reinterpret_cast<uint64_t>(cur.row ? cur.row + k_at : a.hot);
       const int rows = min(per, max(0, ((cn + 31) & ~31) - pw * per));
-      const int total = rows * cpr;
+      const uint32_t st = base + s * a.stage_bytes + pw * per * 128;
+      for (int col0 = 0; col0 < cpr;) {
+        const int left = cpr - col0, lw = left >= 32 ? 5 : 31 - __clz(left);
+        const int tl = lane >> lw, col = col0 + (lane & ((1 << lw) - 1));
+        const bool is_k = col < kc;
+        const int j = is_k ? col : col - kc;
+        const int64_t src_off = 16 * col + (is_k ? 0 : v_at);
+        const uint32_t dst_off = st + ((is_k ? 0 : a.k_chunks) + (j >> 3)) * a.tile * 128;
 #pragma unroll 4
-      for (int i0 = 0; i0 < total; i0 += 32) {
-        const int idx = i0 + lane;
-        uint32_t t, ch;
-        by_row.divmod(idx, t, ch);
-        const char *src = reinterpret_cast<const char *>(__shfl_sync(0xffffffffu, row, t & 31));
-        if (idx < total) {
-          const uint32_t tt = pw * per + t;
-          const bool is_k = static_cast<int>(ch) < kc;
-          const uint32_t vch = ch - kc;
-          const uint32_t dst = st + (is_k ? (ch >> 3) * a.tile : (a.k_chunks + (vch >> 3)) * a.tile) * 128 +
-                               tt * 128 + (((is_k ? ch : vch) & 7 ^ (tt & 7)) << 4);
-          cp_async16(dst, src ? src + (is_k ? k_at : v_at) + 16 * ch : a.hot, src ? 16 : 0);
+        for (int tb = 0; tb < rows; tb += 32 >> lw) {
+          const int t = tb + tl;
+          const uint64_t src = __shfl_sync(0xffffffffu, row, t & 31);
+          const bool ok = have >> (t & 31) & 1;
+          if (t < rows)
+            cp_async16(dst_off + t * 128 + ((j & 7 ^ (t & 7)) << 4),
+                       reinterpret_cast<const char *>(src) + (ok ? src_off : 0), ok ? 16 : 0);
         }
+        col0 += 1 << lw;
       }
       cp_commit();
       cur = ahead;
@@ -645,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
       if (issued < tiles) {
         const uint32_t bar = b_empty + 8 * (issued % a.stages), parity = (issued / a.stages - 1) & 1;
         if (issued == signalled) bar_wait(bar, parity, fail);
-        go = issued == signalled || __all_sync(0xffffffffu, bar_try(bar, parity));
+        go = issued == signalled || __all_sync(0xffffffffu, bar_test(bar, parity));
       }
       if (go) {
         issue();
@@ -653,121 +700,164 @@ __global__ void __launch_bounds__(kThreads, N == 16 ? 2 : 1) attend_kernel(const
         signal();
       }
     }
-  } else if (lane == 0) {
-    // ---- products ------------------------------------------------------------------
+  } else {
+    // ---- products: the whole warp walks the loops, one lane issues -------------------
     const uint32_t d_qk = mma_desc(N, false, false);
     const uint32_t d_pv = mma_desc(N, false, true), d_pv5 = mma_desc(N, true, true);
     const int k_steps = (a.k_dim + 31) >> 5;
+    const uint32_t elected = elect_one();
+    const uint32_t q_desc = smem_desc(base + a.off_q), p_desc = smem_desc(base + a.off_p);
     bar_wait(b_q, 0, fail);
     auto scores = [&](int i) {
       const int s = i % a.stages;
       bar_wait(b_full + 8 * s, (i / a.stages) & 1, fail);
+      __syncwarp();
       tc_after();
-      const uint32_t st = base + s * a.stage_bytes;
       const uint32_t d = tmem + (i & 1) * N;
-      uint32_t acc = 0;
-      for (int t = 0; t < kTerms; ++t)
-        for (int k = 0; k < k_steps; ++k) {
-          const int c = k >> 2, off = (k & 3) * 32;
-          mma_f8(d, smem_desc(st + c * a.tile * 128 + off),
-                 smem_desc(base + a.off_q + (t * a.k_chunks + c) * N * 128 + off), d_qk, acc);
-          acc = 1;
+      uint32_t q = q_desc;
+      for (int t = 0; t < kTerms; ++t) {
+        uint32_t k = smem_desc(base + s * a.stage_bytes);
+        for (int left = k_steps; left > 0; left -= 4) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e < left) mma_f8(d, k + 2 * e, q + 2 * e, d_qk, t > 0 || left < k_steps || e > 0, elected);
+          k += a.tile * 8;
+          q += N * 8;
         }
-      tc_commit(b_s + 8 * (i & 1));
+      }
+      tc_commit(b_s + 8 * (i & 1), elected);
     };
     if (tiles > 0) scores(0);
     for (int i = 0; i < tiles; ++i) {
       if (i + 1 < tiles) scores(i + 1);
       const int s = i % a.stages, cn = min(a.tile, t1 - t0 - i * a.tile);
       bar_wait(b_p, i & 1, fail);
+      __syncwarp();
       tc_after();
-      const uint32_t v = base + s * a.stage_bytes + (a.latent ? 0 : a.k_chunks * a.tile * 128);
+      uint32_t v = smem_desc(base + s * a.stage_bytes + (a.latent ? 0 : a.k_chunks * a.tile * 128));
       const int steps = (cn + 31) >> 5;
-      for (int j = 0; j < a.v_tiles; ++j)
+      for (int j = 0; j < a.v_tiles; ++j) {
         for (int k = 0; k < steps; ++k)
 #pragma unroll
           for (int t = 0; t < kTerms; ++t)
-            mma_f8(t_o + j * N, smem_desc(v + j * a.tile * 128 + k * 4096),
-                   smem_desc(base + a.off_p + k * 4096 + t * N), t + 1 < kTerms ? d_pv : d_pv5,
-                   i > 0 || k > 0 || t > 0);
-      tc_commit(b_empty + 8 * s);
-      tc_commit(b_pv);
+            mma_f8(t_o + j * N, v + k * 256, p_desc + k * 256 + t * N / 16,
+                   t + 1 < kTerms ? d_pv : d_pv5, i > 0 || k > 0 || t > 0, elected);
+        v += a.tile * 8;
+      }
+      tc_commit(b_empty + 8 * s, elected);
+      tc_commit(b_pv, elected);
     }
   }
   // ---- join ----------------------------------------------------------------------
-  // Every product has been read back into order by the softmax warps' last wait; the stages
-  // and Q hold nothing any more, and take the CTA's sums [N][v_dim].
+  // Every product is done (the softmax warps' last wait), so the stages and Q hold
+  // nothing any more.  A lone CTA writes its results from TMEM; in a cluster they take the
+  // CTA's sums [N][v_dim] for the others to read.
   __syncwarp();
   __syncthreads();
-  if (warp < kSoft && tiles > 0) {
+  T *out = static_cast<T *>(a.out) + qrow * a.out_row;
+  const int h0 = kvh * a.group + hg * N, heads = min(N, a.group - static_cast<int>(hg) * N);
+  if (warp < kSoft) {
     tc_after();
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const int grp = warp >> 2, wl = warp & 3, c0 = grp * NC;
+    const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
     for (int j = 0; j < a.v_tiles; ++j) {
-      const int d = j * 128 + warp * 32 + lane;
+      const int d = j * 128 + wl * 32 + lane;
+      float o[NC];
+      if (tiles > 0) {
 #pragma unroll
-      for (int c = 0; c < N; c += 16) {
-        uint32_t o[16];
-        tc_ld16(t_o + lanes + j * N + c, o);
-        tc_wait_ld16(o);
-        if (d < a.v_dim) {
+        for (int c = 0; c < NC; c += 16)
+          tc_ld16(t_o + lanes + j * N + c0 + c, reinterpret_cast<uint32_t *>(o + c));
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((c + e) * a.v_dim + d) * 4), "r"(o[e])
-                         : "memory");
+        for (int c = 0; c < NC; c += 16) tc_wait_ld16(reinterpret_cast<uint32_t *>(o + c));
+      } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) o[c] = 0.f;
+      }
+      if (d >= a.v_dim) continue;
+      if (a.cluster == 1) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float f = s_f[c0 + c];
+          if (c0 + c < heads)
+            out[static_cast<int64_t>(h0 + c0 + c) * a.out_head + d] = from_f32<T>(f != 0.f ? o[c] * f : 0.f);
         }
+      } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c0 + c) * a.v_dim + d) * 4), "f"(o[c]) : "memory");
       }
     }
+    __syncwarp();
     tc_before();
   }
-  __syncthreads();
-  if (warp == kSoft + kGather) {
+  if (a.cluster == 1) {
+    if (a.lse && tid < heads) {
+      const float z = s_l[tid];
+      a.lse[qrow * a.heads + h0 + tid] =
+          z > 0.f || z != z ? (s_m[tid] + log2f(z)) * 0.6931471805599453f : -INFINITY;
+    }
+    __syncthreads();
+  } else {
+    __syncwarp();
+    cluster_sync();
+  }
+  if (warp == kWorkers) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(a.tmem_cols));
   }
-  if (a.cluster > 1) cluster_sync();
+  if (tid == 0 && s_fail && a.status) atomicOr(a.status, HISPARSE_ERR_WAIT);
+  if (a.cluster == 1) return;
   // Each CTA joins a share of the heads: weights 2^(m_r - max m) of the CTAs' sums.
   const int share = N / a.cluster, n0 = static_cast<int>(rank) * share;
   if (tid < share) {
     const int n = n0 + tid;
-    float m = -INFINITY;
-    for (int r = 0; r < a.cluster; ++r) m = fmaxf(m, ld_peer(peer(smem_u32(&s_m[n]), r)));
-    float z = 0.f;
+    float m = -INFINITY, z = 0.f;
+#pragma unroll 4
     for (int r = 0; r < a.cluster; ++r) {
-      const float mr = ld_peer(peer(smem_u32(&s_m[n]), r));
-      const float w = mr > -INFINITY ? ex2(mr - m) : 0.f;
-      s_w[r * N + tid] = w;
-      if (w > 0.f || w != w) z = fmaf(w, ld_peer(peer(smem_u32(&s_l[n]), r)), z);
+      const float x = ld_peer(peer(smem_u32(&s_m[n]), r));
+      s_w[r * N + tid] = x;
+      m = fmaxf(m, x);
     }
-    s_f[tid] = z > 0.f || z != z ? 1.f / z : 0.f;
-    const int h = static_cast<int>(hg) * N + n;
-    if (a.lse && h < a.group)
-      a.lse[qrow * a.heads + kvh * a.group + h] = z > 0.f || z != z ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll 4
+    for (int r = 0; r < a.cluster; ++r) {
+      const float x = s_w[r * N + tid], y = ld_peer(peer(smem_u32(&s_l[n]), r));
+      const float w = x > -INFINITY ? ex2(x - m) : 0.f;
+      s_w[r * N + tid] = w;
+      z = fmaf(w, y, z);
+    }
+    s_qf[tid] = z > 0.f || z != z ? 1.f / z : 0.f;
+    if (a.lse && n < heads)
+      a.lse[qrow * a.heads + h0 + n] = z > 0.f || z != z ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
   }
   __syncthreads();
-  T *out = static_cast<T *>(a.out) + qrow * a.out_row;
-  const int quads = a.v_dim >> 2;
-  for (int i = tid; i < share * quads; i += kThreads) {
-    const int nn = i / quads, d = (i - nn * quads) * 4;
-    const int h = static_cast<int>(hg) * N + n0 + nn;
-    if (h >= a.group) continue;
+  for (uint32_t i = tid; i < share * a.quads.d; i += kThreads) {
+    uint32_t nn, d;
+    a.quads.divmod(i, nn, d);
+    if (n0 + static_cast<int>(nn) >= heads) continue;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const uint32_t at = base + ((n0 + nn) * a.v_dim + d) * 4;
-    for (int r = 0; r < a.cluster; ++r) {
-      const float w = s_w[r * N + nn];
-      if (w == 0.f) continue;  // nothing there, or nothing of weight: its sums are not read
-      const float4 v = ld_peer4(peer(at, r));
-      acc[0] = fmaf(w, v.x, acc[0]);
-      acc[1] = fmaf(w, v.y, acc[1]);
-      acc[2] = fmaf(w, v.z, acc[2]);
-      acc[3] = fmaf(w, v.w, acc[3]);
+    const uint32_t at = base + ((n0 + nn) * a.v_dim + 4 * d) * 4;
+#pragma unroll 1
+    for (int r0 = 0; r0 < a.cluster; r0 += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r0 + r < a.cluster) v[r] = ld_peer4(peer(at, r0 + r));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r0 + r >= a.cluster) break;
+        const float w = s_w[(r0 + r) * N + nn];
+        acc[0] = fmaf(w, v[r].x, acc[0]);
+        acc[1] = fmaf(w, v[r].y, acc[1]);
+        acc[2] = fmaf(w, v[r].z, acc[2]);
+        acc[3] = fmaf(w, v[r].w, acc[3]);
+      }
     }
-    const float inv = s_f[nn];
+    const float inv = s_qf[nn];
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = inv != 0.f ? acc[e] * inv : 0.f;
-    store_vec<T, 4>(out + static_cast<int64_t>(kvh * a.group + h) * a.out_head + d, acc);
+    store_vec<T, 4>(out + static_cast<int64_t>(h0 + n0 + nn) * a.out_head + 4 * d, acc);
   }
-  if (tid == 0 && s_fail && a.status) atomicOr(a.status, HISPARSE_ERR_WAIT);
-  if (a.cluster > 1) cluster_sync();  // peers have read this CTA's shared memory
+  cluster_sync();  // peers have read this CTA's shared memory
 }
 
 constexpr uint32_t kSmemSm = 233472;     // of an SM; a CTA takes its own and 1 KB more
@@ -840,7 +930,7 @@ int launch_attend(AttendArgs a, int64_t units, void *stream) {
   a.cluster = c;
   a.per_cta = static_cast<int>(((tokens + c - 1) / c + 31) / 32 * 32);
   if (units * c > 0x7fffffff) return HISPARSE_EBOUND;
-  return launch_pdl(fn, dim3(static_cast<unsigned>(units * c)), dim3(kThreads), bytes, stream, c, a);
+  return launch_pdl(fn, dim3(static_cast<unsigned>(units * c)), dim3(Shape<N>::threads), bytes, stream, c, a);
 }
 
 template <class T>
@@ -906,7 +996,7 @@ int hisparse_attend(const hisparse_attend_args *g, void *stream) {
   a.scales = g->scales; a.scales_req = g->scales_req_stride; a.scale_blocks = g->scale_blocks;
   a.seq_lens = g->d_seq_lens; a.num_reqs = g->d_num_reqs; a.status = g->d_status;
   a.row_bytes = row;
-  a.by_row = FastDiv((r.k_dim + (r.latent ? 0 : r.v_dim)) / 16);
+  a.quads = FastDiv(r.v_dim / 4);
   const int64_t pairs = static_cast<int64_t>(g->num_requests) * g->rows * r.kv_heads;
   return g->dtype == HISPARSE_BF16 ? pick_attend<__nv_bfloat16>(a, pairs, stream)
                                    : pick_attend<__half>(a, pairs, stream);
