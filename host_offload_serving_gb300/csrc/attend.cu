@@ -18,23 +18,27 @@
 // (p_j sV_j is what multiplies the raw bytes of V), through the exponent, so the
 // running maximum is over s_j + log2(sV_j) and no product leaves the range.
 //
-// Warps: four softmax warps (a lane a token, TMEM lane = token) for each 32 columns, four that
-// gather (16-byte cp.async into the 128-byte-swizzled tiles the tensor cores read,
-// several tiles ahead), and one that issues the products.  S is double buffered in TMEM, so the scores of tile i+1
+// Warps: four softmax warps (a lane a token, TMEM lane = token) for each 32 columns; six or
+// eight that gather (16-byte cp.async into the 128-byte-swizzled tiles that the tensor cores
+// read, several tiles ahead); one or two that turn slots and positions into addresses and scales;
+// and one that issues the products.  S is double buffered in TMEM, so the scores of tile i+1
 // are computed while the softmax of tile i runs.  O is rescaled only where a column's
 // maximum has grown by more than 2^2.75 since it was last set.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 
 #include "common.cuh"
 
 namespace {
 
-constexpr int kGather = 4;  // warps that gather
+constexpr int kTables = 4;  // tiles whose rows' addresses and scales are known ahead
 constexpr int kMaxStages = 6;
 constexpr int kMaxCluster = 16;
-constexpr float kTop = 6.f;     // log2 of a column's largest probability when its offset is set
-constexpr float kSlack = 8.75f; // ... and what it may grow to before the offset moves (448 = 2^8.8)
+constexpr float kNone = -1e30f; // a CTA's offset where it had no token
+// log2 of a column's largest probability when its offset is set, and what it may grow to before
+// the offset moves again (the largest e4m3 is 448 = 2^8.8).
+constexpr float kTop = 6.f, kSlack = 8.75f;
 
 struct AttendArgs {
   int32_t rows, entries, heads, kv_heads, k_dim, v_dim, latent, B;
@@ -60,7 +64,7 @@ struct AttendArgs {
   // the launch's plan
   int32_t cluster, per_cta, tile, stages, k_chunks, v_chunks, v_tiles, tmem_cols;
   FastDiv quads;  // v_dim / 4
-  uint32_t stage_bytes, off_q, off_p, off_meta, off_misc;
+  uint32_t stage_bytes, off_q, off_p, off_meta, off_rows;
 };
 
 // ---- PTX ---------------------------------------------------------------------
@@ -155,10 +159,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(elected), "r"(kDescHi)
       : "memory");
 }
-#define TC_REGS16(r)                                                                        \
-  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),   \
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),     \
-      "r"(r[15])
 __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t *r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -171,8 +171,9 @@ __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t *r) {
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::TC_REGS16(r),
-      "r"(addr)
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]), "r"(r[1]),
+      "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
 // Waits for the loads before it; the values pass through it, so nothing that uses them moves
@@ -188,11 +189,11 @@ __device__ __forceinline__ void tc_wait_ld16(uint32_t *r) {
 __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// 16 bytes of global memory into shared memory, or 16 zeros where `bytes` is 0.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const char *src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, uint64_t src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// What a masked token's row reads: zeros, as its probability is 0 and 0 * NaN is not.
+__device__ uint4 g_zeros[640 / 16];
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_wait(int pending) {
   switch (pending) {
@@ -214,19 +215,31 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// OR over a group of four softmax warps, and their barrier.
-__device__ __forceinline__ bool soft_any(int group, bool x) {
+// OR over a group of four softmax warps, and their barrier (1 or 2: constants, as a CTA
+// takes all 16 hardware barriers for one that is not, and two such CTAs do not fit an SM).
+template <int kId>
+__device__ __forceinline__ bool any_of_128(bool x) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n"
       " barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x)), "r"(group + 1)
+      : "r"(static_cast<uint32_t>(x)), "n"(kId)
       : "memory");
   return r != 0;
 }
+template <int kGroups>
+__device__ __forceinline__ bool soft_any(int group, bool x) {
+  if (kGroups == 1 || group == 0) return any_of_128<1>(x);
+  return any_of_128<2>(x);
+}
+template <int kGroups>
 __device__ __forceinline__ void soft_sync(int group) {
-  asm volatile("barrier.cta.sync %0, 128;" ::"r"(group + 1) : "memory");
+  if (kGroups == 1 || group == 0) {
+    asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+  } else {
+    asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
+  }
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
@@ -245,6 +258,14 @@ __device__ __forceinline__ float ld_peer(uint32_t addr) {
 __device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
   float4 r;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+               : "r"(addr)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ float4 ld_shared4(uint32_t addr) {
+  float4 r;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
                : "r"(addr)
                : "memory");
@@ -273,13 +294,104 @@ __device__ __forceinline__ uint32_t take_term(float &x, float &y) {
   return p;
 }
 
+// The largest magnitude of 24 values (NaN left out).
+template <class T>
+__device__ __forceinline__ float abs_max(const uint4 (&v)[3]);
+template <>
+__device__ __forceinline__ float abs_max<__nv_bfloat16>(const uint4 (&v)[3]) {
+  __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const __nv_bfloat162 *e = reinterpret_cast<const __nv_bfloat162 *>(&v[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = __hmax2(m, __habs2(e[j]));
+  }
+  return fmaxf(__low2float(m), __high2float(m));
+}
+template <>
+__device__ __forceinline__ float abs_max<__half>(const uint4 (&v)[3]) {
+  __half2 m = __float2half2_rn(0.f);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const __half2 *e = reinterpret_cast<const __half2 *>(&v[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = __hmax2(m, __habs2(e[j]));
+  }
+  return fmaxf(__low2float(m), __high2float(m));
+}
+// 8 values times `up` as e4m3 terms; word 0 holds the terms of the first four.
+template <class T, int kTerms>
+__device__ __forceinline__ void split8(const uint4 &v, float up, uint32_t (&w0)[kTerms], uint32_t (&w1)[kTerms]) {
+  const T *e = reinterpret_cast<const T *>(&v);
+  if constexpr (kTerms == 2) {
+    // |x| < 256: in f16, 11 significant bits against the 8 of the values, and as far down as
+    // the second term reaches.
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float x = to_f32<T>(e[2 * j]) * up, y = to_f32<T>(e[2 * j + 1]) * up;
+      uint32_t h, back;
+      uint16_t p, r;
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(p) : "r"(h));
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(p));
+      const __half2 left = __hsub2(*reinterpret_cast<__half2 *>(&h), *reinterpret_cast<__half2 *>(&back));
+      asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&left)));
+      hi[j] = p;
+      lo[j] = r;
+    }
+    w0[0] = hi[0] | hi[1] << 16;
+    w1[0] = hi[2] | hi[3] << 16;
+    w0[1] = lo[0] | lo[1] << 16;
+    w1[1] = lo[2] | lo[3] << 16;
+  } else {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = to_f32<T>(e[j]) * up;
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t) {
+      w0[t] = take_term<false>(x[0], x[1]);
+      w0[t] |= take_term<false>(x[2], x[3]) << 16;
+      w1[t] = take_term<false>(x[4], x[5]);
+      w1[t] |= take_term<false>(x[6], x[7]) << 16;
+    }
+  }
+}
+
+// 2^kLw columns of 16-byte chunks of a warp's share of the rows: lane t * 2^kLw + c copies
+// chunk c of row t of a turn.  The rows' addresses are a table in shared memory (8 bytes a
+// row); `dst` is the lane's place in row 0 of a 128-byte-swizzled tile, whose 16-byte
+// chunk is XORed with the row's lowest 3 bits.  A warp takes every kWarps-th group of 8 rows.
+template <int kLw, int kWarps>
+__device__ __forceinline__ void gather_columns(uint32_t table, uint32_t off, uint32_t dst, int groups, int warp,
+                                               int lane) {
+  constexpr int kDt = 32 >> kLw;                  // rows in one turn of the warp
+  constexpr int kTurns = kDt < 8 ? 8 / kDt : 1;   // turns in a group of 8 rows
+  constexpr int kAtOnce = kDt <= 8 ? 1 : kDt / 8; // groups in one turn
+  const int tl = lane >> kLw;
+  const int sub = kAtOnce > 1 ? tl >> 3 : 0;      // the group of a turn that the lane is in
+  const int row = kAtOnce > 1 ? tl & 7 : tl;
+#pragma unroll 1
+  for (int g = warp; g < groups; g += kWarps * kAtOnce) {
+    const int mine = g + sub * kWarps;
+    if (kAtOnce > 1 && mine >= groups) continue;
+    const uint32_t src = table + (mine * 8 + row) * 8;
+    const uint32_t to = (dst ^ ((row & 7) << 4)) + (mine * 8 + row) * 128;
+    uint64_t p[kTurns];
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) asm volatile("ld.shared.b64 %0, [%1];" : "=l"(p[u]) : "r"(src + u * kDt * 8));
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) cp_async16((to ^ (u * kDt << 4)) + u * kDt * 128, p[u] + off);
+  }
+}
+
 // ---- tokens ------------------------------------------------------------------
 struct Raw {
   int32_t slot, sel, entry;
 };
 struct Token {
   const char *row;  // NULL: nothing to read
-  float k, v;       // the scales
+  const float *scales;
 };
 
 template <class T>
@@ -287,10 +399,14 @@ struct Terms;
 template <>
 struct Terms<__nv_bfloat16> {
   static constexpr int n = 2;
+  // Where more tiles follow they are left room; 2^-8 of the largest is still a normal e4m3, and a
+  // softmax has little of its mass below (2^-4.2 is the centre for 2048 normal scores at worst).
+  static constexpr float top = 2.f;
 };
 template <>
 struct Terms<__half> {
   static constexpr int n = 3;
+  static constexpr float top = kTop;  // (its second term would lose bits at 2^-7 of it)
 };
 
 // Sums of l[0 .. N) over the warp's lanes: at each step a lane hands over half of its
@@ -316,25 +432,32 @@ struct Shape {
   static constexpr int groups = N > 32 ? N / 32 : 1;  // of four softmax warps
   static constexpr int cols = N / groups;             // columns of a softmax thread
   static constexpr int soft = 4 * groups;             // softmax warps
-  static constexpr int workers = soft + kGather;
-  static constexpr int threads = 32 * (workers + 1);
+  static constexpr int gather = N > 32 ? 6 : 8;       // warps that copy rows
+  static constexpr int mma = soft + gather;           // the warp that issues products
+  static constexpr int look = mma + 1;                // warps that look the rows up
+  static constexpr int looks = N > 32 ? 1 : 2;
+  static constexpr int threads = 32 * (look + looks);
 };
 
 template <class T, int N>
-__global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(Shape<N>::threads, 1)
+    attend_kernel(const AttendArgs a) {
   constexpr int kTerms = Terms<T>::n;
-  constexpr int NC = Shape<N>::cols, kSoft = Shape<N>::soft, kWorkers = Shape<N>::workers;
+  constexpr int NC = Shape<N>::cols, kSoft = Shape<N>::soft, kGather = Shape<N>::gather;
   constexpr int kThreads = Shape<N>::threads;
+  constexpr int kQ = kTerms * N;  // rows of Q: the terms of a head are N rows apart
   extern __shared__ char smem_raw[];
-  __shared__ uint64_t s_bars[2 * kMaxStages + 5];
+  __shared__ uint64_t s_bars[2 * kMaxStages + 3 * kTables + 5];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
-  __shared__ float s_m[N], s_l[N], s_f[N], s_wmax[4][N], s_w[kMaxCluster * N];
-  __shared__ __align__(16) float s_qf[N];
+  __shared__ float s_l[N], s_f[N], s_d[N], s_wmax[4][N], s_w[kMaxCluster * N];
+  __shared__ __align__(16) float s_qf[N], s_m[N];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = smem_u32(s_bars);
   const uint32_t b_full = bars, b_empty = bars + 8 * kMaxStages, b_s = bars + 16 * kMaxStages;
   const uint32_t b_p = b_s + 16, b_pv = b_s + 24, b_q = b_s + 32;
+  const uint32_t b_tab = b_s + 40, b_meta = b_tab + 8 * kTables,
+                 b_used = b_meta + 8 * kTables;  // addresses and scales: written; done with
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = a.cluster > 1 ? blockIdx.x % a.cluster : 0;
   const uint32_t unit = blockIdx.x / a.cluster;
@@ -351,11 +474,16 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
     bar_init(b_s + 8, 1);
     bar_init(b_p, 32 * kSoft);
     bar_init(b_pv, 1);
-    bar_init(b_q, 32 * kWorkers);
+    bar_init(b_q, 32 * (kSoft + kGather));
+    for (int t = 0; t < kTables; ++t) {
+      bar_init(b_tab + 8 * t, 32 * Shape<N>::looks);
+      bar_init(b_meta + 8 * t, 32 * Shape<N>::looks);
+      bar_init(b_used + 8 * t, 1);
+    }
     s_fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int c = tid; c < N; c += kThreads) s_m[c] = -INFINITY;
+  for (int c = tid; c < N; c += kThreads) s_m[c] = 0.f;
   // The last 16 of 32 K columns that a product reads beyond k_dim: zero in every
   // stage (the gather never writes them) and in Q.
   if (a.k_dim & 16) {
@@ -364,15 +492,14 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
       const int s = i / a.tile, t = i - s * a.tile;
       st_shared4(base + s * a.stage_bytes + (c * a.tile + t) * 128 + ((j ^ (t & 7)) << 4), 0, 0, 0, 0);
     }
-    for (int i = tid; i < kTerms * N; i += kThreads) {
-      const int n = i % N, term = i / N;
-      st_shared4(base + a.off_q + ((term * a.k_chunks + c) * N + n) * 128 + ((j ^ (n & 7)) << 4), 0, 0, 0, 0);
+    for (int i = tid; i < kQ; i += kThreads) {
+      st_shared4(base + a.off_q + (c * kQ + i) * 128 + ((j ^ (i & 7)) << 4), 0, 0, 0, 0);
     }
     fence_async();
   }
   pdl_wait();
   if (a.num_reqs && req >= *a.num_reqs) return;  // the whole cluster
-  if (warp == kWorkers) {
+  if (warp == Shape<N>::mma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                  "r"(a.tmem_cols)
                  : "memory");
@@ -383,7 +510,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
   tc_after();
   pdl_launch();
   const uint32_t tmem = s_tmem;
-  const uint32_t t_o = tmem + 2 * N;
+  const uint32_t t_o = tmem + 2 * kQ;
 
   const int ntok = a.entries * static_cast<int>(a.rec_tokens.d);
   const int t0 = min(ntok, static_cast<int>(rank) * a.per_cta), t1 = min(ntok, t0 + a.per_cta);
@@ -391,18 +518,18 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
   const int64_t entry0 = qrow * a.entries;
   volatile int *fail = &s_fail;
 
-  // Query heads of this group into e4m3 terms, a warp a head in turn of the workers.
+  // Query heads of this group into e4m3 terms, by the softmax and gather warps while the
+  // first rows are looked up.
   auto make_q = [&](int w) {
     const int vecs = a.k_dim >> 3;
     const T *q0 = static_cast<const T *>(a.q) + qrow * a.q_row;
-    constexpr int kTurns = (N + kWorkers - 1) / kWorkers;
-    constexpr int kBatch = kTurns < 3 ? kTurns : kTurns == 4 ? 4 : 3;
-#pragma unroll 1
-    for (int n0 = w; n0 < N; n0 += kWorkers * kBatch) {
-      uint4 v[kBatch][3];
+    constexpr int kWarps = kSoft + kGather, kBatch = (N + kWarps - 1) / kWarps;
+    {
+      const int n0 = w;
+      uint4 v[kBatch][3];  // all of a warp's heads in flight together
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int n = n0 + kWorkers * b, h = static_cast<int>(hg) * N + n;
+        const int n = n0 + kWarps * b, h = static_cast<int>(hg) * N + n;
         const uint4 *src = reinterpret_cast<const uint4 *>(q0 + static_cast<int64_t>(kvh * a.group + h) * a.q_head);
 #pragma unroll
         for (int i = 0; i < 3; ++i)
@@ -410,16 +537,9 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
       }
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int n = n0 + kWorkers * b;
+        const int n = n0 + kWarps * b;
         if (n >= N) break;
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const T *e = reinterpret_cast<const T *>(&v[b][i]);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(to_f32<T>(e[j])));
-        }
-        m = warp_max(m);
+        const float m = warp_max(abs_max<T>(v[b]));
         // q * 2^sh has its largest in [128, 256)
         const int ex = static_cast<int>(__float_as_uint(m) >> 23) - 127;
         const int sh = m > 0.f ? min(7 - ex, 120) : 0;
@@ -431,22 +551,14 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
         for (int i = 0; i < 3; ++i) {
           if (32 * i >= vecs) break;
           if (lane + 32 * i >= vecs) continue;
-          const T *e = reinterpret_cast<const T *>(&v[b][i]);
-          float x[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = to_f32<T>(e[j]) * up;
           const int d = (lane + 32 * i) * 8;
-          const uint32_t at = ((d >> 7) * N + n) * 128 + (((d & 127) >> 4 ^ (n & 7)) << 4) + (d & 15);
+          const uint32_t at = base + a.off_q + ((d >> 7) * kQ + n) * 128 + (((d & 127) >> 4 ^ (n & 7)) << 4) + (d & 15);
+          uint32_t w0[kTerms], w1[kTerms];
+          split8<T>(v[b][i], up, w0, w1);
 #pragma unroll
-          for (int t = 0; t < kTerms; ++t) {
-            uint32_t w0 = take_term<false>(x[0], x[1]);
-            w0 |= take_term<false>(x[2], x[3]) << 16;
-            uint32_t w1 = take_term<false>(x[4], x[5]);
-            w1 |= take_term<false>(x[6], x[7]) << 16;
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(base + a.off_q + t * a.k_chunks * N * 128 + at),
-                         "r"(w0), "r"(w1)
+          for (int t = 0; t < kTerms; ++t)
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + t * N * 128), "r"(w0[t]), "r"(w1[t])
                          : "memory");
-          }
         }
       }
     }
@@ -465,16 +577,17 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
     const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
     const int tk = wl * 32 + lane;
     const uint32_t p_row = base + a.off_p + tk * 128;
+    bool seen = false;  // some token so far
     for (int i = 0; i < tiles; ++i) {
-      const int s = i % a.stages, cn = min(a.tile, t1 - t0 - i * a.tile);
-      bar_wait(b_full + 8 * s, (i / a.stages) & 1, fail);
+      const int cn = min(a.tile, t1 - t0 - i * a.tile);
+      bar_wait(b_meta + 8 * (i % kTables), (i / kTables) & 1, fail);
       float ks = 0.f, lv = 0.f, iv = 1.f;
       bool use = false;
       if (tk < cn) {
         float2 meta;
         asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
                      : "=f"(meta.x), "=f"(meta.y)
-                     : "r"(base + a.off_meta + (s * a.tile + tk) * 8)
+                     : "r"(base + a.off_meta + (i % kTables * a.tile + tk) * 8)
                      : "memory");
         use = __float_as_int(meta.x) != 0x7fffffff;
         if (use) {
@@ -488,47 +601,67 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
       __syncwarp();
       tc_after();
       float x[NC];
+      {
+        const uint32_t at = tmem + lanes + (i & 1) * kQ + c0;
 #pragma unroll
-      for (int c = 0; c < NC; c += 16)
-        tc_ld16(tmem + lanes + (i & 1) * N + c0 + c, reinterpret_cast<uint32_t *>(x + c));
+        for (int c = 0; c < NC; c += 16) {
+          float y[kTerms][16];
 #pragma unroll
-      for (int c = 0; c < NC; c += 16) tc_wait_ld16(reinterpret_cast<uint32_t *>(x + c));
-      // scores in powers of two, the V scale in them
-      float mine = -INFINITY;  // lane c keeps the maximum of column c
+          for (int t = 0; t < kTerms; ++t) tc_ld16(at + t * N + c, reinterpret_cast<uint32_t *>(y[t]));
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        x[c] = use ? fmaf(x[c] * ks, s_qf[c0 + c], lv) : -INFINITY;
-        const float m = warp_max(x[c]);
-        if (lane == c) mine = m;
-      }
-      if (lane < NC) s_wmax[wl][c0 + lane] = mine;
-      soft_sync(grp);
-      bool moved = false;
-      if (gt < NC) {
-        const int c = c0 + gt;
-        const float m = fmaxf(fmaxf(s_wmax[0][c], s_wmax[1][c]), fmaxf(s_wmax[2][c], s_wmax[3][c]));
-        const float old = s_m[c];
-        float f = 1.f;
-        if (m > -INFINITY && !(m - old <= kSlack)) {
-          f = old > -INFINITY ? ex2(old - (m - kTop)) : 0.f;
-          s_m[c] = m - kTop;
-          moved = true;
+          for (int t = 0; t < kTerms; ++t) tc_wait_ld16(reinterpret_cast<uint32_t *>(y[t]));
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            x[c + e] = y[0][e] + y[1][e];
+            if (kTerms == 3) x[c + e] += y[kTerms - 1][e];
+          }
         }
-        s_f[c] = f;
       }
-      moved = soft_any(grp, moved);
-      if (i > 0) {
-        bar_wait(b_pv, (i - 1) & 1, fail);  // O and the probabilities' buffer are free
-        __syncwarp();
-        tc_after();
-      }
-      if (moved) {
+      // scores in powers of two, the V scale in them, above their column's offset
+      float most = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) l[c] *= s_f[c0 + c];
+      for (int c = 0; c < NC; c += 4) {
+        const float4 f = ld_shared4(smem_u32(s_qf + c0 + c)), m = ld_shared4(smem_u32(s_m + c0 + c));
+        const float g[4] = {f.x, f.y, f.z, f.w}, o[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[c + e] = use ? fmaf(x[c + e] * ks, g[e], lv - o[e]) : -INFINITY;
+          most = fmaxf(most, x[c + e]);
+        }
+      }
+      const bool moved = soft_any<Shape<N>::groups>(grp, most > kSlack || (!seen && most > -INFINITY));
+      auto previous = [&] {  // O and the probabilities' buffer are free
         if (i > 0) {
-          for (int j = 0; j < a.v_tiles; ++j)
+          bar_wait(b_pv, (i - 1) & 1, fail);
+          __syncwarp();
+          tc_after();
+        }
+      };
+      if (moved) {  // some columns outgrew their offset: new offsets, and their sums follow
+        float mine = -INFINITY;  // lane c keeps the maximum of column c
 #pragma unroll
-            for (int c = 0; c < NC; c += 16) {
+        for (int c = 0; c < NC; ++c) {
+          const float m = warp_max(x[c]);
+          if (lane == c) mine = m;
+        }
+        if (lane < NC) s_wmax[wl][c0 + lane] = mine;
+        soft_sync<Shape<N>::groups>(grp);
+        if (gt < NC) {
+          const int c = c0 + gt;
+          const float m = fmaxf(fmaxf(s_wmax[0][c], s_wmax[1][c]), fmaxf(s_wmax[2][c], s_wmax[3][c]));
+          const float d = m > kSlack || (!seen && m > -INFINITY) ? m - (tiles == 1 ? kTop : Terms<T>::top) : 0.f;
+          s_d[c] = d;
+          s_f[c] = ex2(-d);
+          s_m[c] += d;
+        }
+        soft_sync<Shape<N>::groups>(grp);
+        previous();
+        if (seen) {
+#pragma unroll 1
+          for (int c = 0; c < NC; c += 16) {
+            if (!__any_sync(0xffffffffu, s_d[c0 + c + (lane & 15)] != 0.f)) continue;
+#pragma unroll 1
+            for (int j = 0; j < a.v_tiles; ++j) {
               uint32_t o[16];
               const uint32_t at = t_o + lanes + j * N + c0 + c;
               tc_ld16(at, o);
@@ -537,15 +670,21 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_f[c0 + c + e]);
               tc_st16(at, o);
             }
+          }
           tc_wait_st();
+#pragma unroll
+          for (int c = 0; c < NC; ++c) l[c] *= s_f[c0 + c];
         }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) x[c] -= s_d[c0 + c];
+        seen = true;
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const float m = s_m[c0 + c];
-        x[c] = ex2(x[c] - (m > -INFINITY ? m : 0.f));
+        x[c] = ex2(x[c]);
         l[c] = fmaf(x[c], iv, l[c]);
       }
+      if (!moved) previous();
       if (tk < ((cn + 31) & ~31)) {
 #pragma unroll
         for (int t = 0; t < kTerms; ++t)
@@ -571,17 +710,18 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
       bar_arrive(b_p);
     }
     column_sums<NC, 16, NC / 2>(l, lane);
-    soft_sync(grp);  // s_wmax is free
+    soft_sync<Shape<N>::groups>(grp);  // s_wmax is free
     if (NC == 32) {
       s_wmax[wl][c0 + lane] = l[0];
     } else if ((lane & 1) == 0) {
       s_wmax[wl][c0 + (lane >> 1)] = l[0];
     }
-    soft_sync(grp);
+    soft_sync<Shape<N>::groups>(grp);
     if (gt < NC) {
       const int c = c0 + gt;
       const float z = (s_wmax[0][c] + s_wmax[1][c]) + (s_wmax[2][c] + s_wmax[3][c]);
       s_l[c] = z;
+      if (!seen) s_m[c] = kNone;
       s_f[c] = z > 0.f || z != z ? 1.f / z : 0.f;
     }
     if (tiles > 0) {
@@ -589,39 +729,102 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
       tc_after();
     }
     __syncwarp();
-  } else if (warp < kWorkers) {
+  } else if (warp < Shape<N>::mma) {
     // ---- gather ------------------------------------------------------------------
-    const int pw = warp - kSoft, per = a.tile / kGather;
-    const int kc = a.k_dim >> 4, cpr = kc + (a.latent ? 0 : a.v_dim >> 4);
+    // Groups of 8 rows in turn, 16-byte chunks of them in passes of a power of two of columns.
+    const int gw = warp - kSoft;
+    const int kc = a.k_dim >> 4, vc = a.latent ? 0 : a.v_dim >> 4;
+    make_q(warp);
+    int issued = 0, signalled = 0;
+    auto issue = [&]() {
+      const int i = issued, s = i % a.stages;
+      const int groups = (min(a.tile, t1 - t0 - i * a.tile) + 31) >> 5 << 2;
+      const uint32_t st = base + s * a.stage_bytes;
+      const uint32_t table = base + a.off_rows + i % kTables * a.tile * 8;
+      for (int part = 0; part < (vc ? 2 : 1); ++part) {
+        const int cols = part ? vc : kc;
+        const uint32_t rows = table + part * kTables * a.tile * 8;
+        for (int col0 = 0; col0 < cols;) {
+          const int left = cols - col0, lw = left >= 32 ? 5 : 31 - __clz(left);
+          const int j = col0 + (lane & ((1 << lw) - 1));
+          const uint32_t dst = st + ((part ? a.k_chunks : 0) + (j >> 3)) * a.tile * 128 + ((j & 7) << 4);
+          switch (lw) {
+            case 5: gather_columns<5, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
+            case 4: gather_columns<4, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
+            case 3: gather_columns<3, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
+            case 2: gather_columns<2, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
+            case 1: gather_columns<1, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
+            default: gather_columns<0, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
+          }
+          col0 += 1 << lw;
+        }
+      }
+      cp_commit();
+      ++issued;
+    };
+    auto signal = [&]() {
+      cp_wait(issued - signalled - 1);
+      fence_async();
+      bar_arrive(b_full + 8 * (signalled % a.stages));
+      ++signalled;
+    };
+    while (signalled < tiles) {
+      bool go = false;
+      if (issued < tiles) {
+        // the stage is free and the rows are known; with nothing in flight, wait for both
+        const bool fresh = issued < a.stages;
+        const uint32_t free = b_empty + 8 * (issued % a.stages), fp = (issued / a.stages - 1) & 1;
+        const uint32_t known = b_tab + 8 * (issued % kTables), kp = (issued / kTables) & 1;
+        go = issued == signalled;
+        if (go) {
+          if (!fresh) bar_wait(free, fp, fail);
+          bar_wait(known, kp, fail);
+        } else {
+          go = __all_sync(0xffffffffu, (fresh || bar_test(free, fp)) && bar_test(known, kp));
+        }
+        __syncwarp();
+      }
+      if (go) {
+        issue();
+      } else {
+        signal();
+      }
+    }
+  } else if (warp >= Shape<N>::look) {
+    // ---- rows: slot -> address, position -> scales, tiles ahead of their copies --------
     const int64_t k_at = static_cast<int64_t>(kvh) * a.k_dim;
-    // from a K head's first byte to where its V head would begin 16 * kc bytes earlier
-    const int64_t v_at = static_cast<int64_t>(a.kv_heads) * a.k_dim + static_cast<int64_t>(kvh) * a.v_dim - 16 * kc - k_at;
+    const int64_t v_at = static_cast<int64_t>(a.kv_heads) * a.k_dim + static_cast<int64_t>(kvh) * a.v_dim;
     const int seq = a.seq_lens ? a.seq_lens[req] : INT32_MAX;
     const float *scales = a.scales + req * a.scales_req + kvh;
     const char *hot = a.hot + req * a.hot_req;
     const int v_col = a.latent ? 0 : a.kv_heads;
-    auto raw = [&](int i) {
-      Raw r = {-1, -1, 0};
-      const int t = t0 + i * a.tile + pw * per + lane;
-      if (lane < per && i < tiles && t < t1) {
-        r.entry = static_cast<int>(a.rec_tokens.div(t));
+    const int64_t sel0 = entry0 / a.sel_block.d;
+    const uint64_t zeros = reinterpret_cast<uint64_t>(g_zeros);
+    const bool plain = a.rec_tokens.d == 1 && a.sel_block.d == 1;  // an entry is a token
+    auto raw = [&](int t) {
+      Raw r = {-1, -1, t};
+      if (t < t1) {
+        if (!plain) r.entry = static_cast<int>(a.rec_tokens.div(t));
         r.slot = a.slots[entry0 + r.entry];
-        r.sel = a.sel_block.d > 1 ? a.sel[entry0 / a.sel_block.d + a.sel_block.div(r.entry)]
-                                  : a.sel[entry0 + r.entry];
+        r.sel = a.sel[plain ? entry0 + t : sel0 + a.sel_block.div(r.entry)];
       }
       return r;
     };
-    auto token = [&](const Raw &r, int i) {
-      Token k = {nullptr, 0.f, 0.f};
+    auto token = [&](const Raw &r, int t) {
+      Token k = {nullptr, nullptr};
       if (r.slot == -1) return k;
-      const int t = t0 + i * a.tile + pw * per + lane;
-      const int sub = t - r.entry * static_cast<int>(a.rec_tokens.d);
-      int64_t pos = r.sel;
-      if (a.sel_block.d > 1 && pos >= 0)
-        pos = pos * a.sel_block.d + (r.entry - a.sel_block.div(r.entry) * a.sel_block.d);
-      pos = pos < 0 ? -1 : pos * a.rec_tokens.d + sub;
-      const int64_t blk = pos <= INT32_MAX ? a.S.div(static_cast<uint32_t>(max(pos, int64_t(0)))) : pos / a.S.d;
-      if (pos >= 0 && blk < a.scale_blocks) {
+      int64_t pos = r.sel, blk;
+      int sub = 0;
+      if (plain) {
+        blk = pos < 0 ? -1 : static_cast<int64_t>(a.S.div(r.sel));
+      } else {
+        sub = t - r.entry * static_cast<int>(a.rec_tokens.d);
+        if (a.sel_block.d > 1 && pos >= 0)
+          pos = pos * a.sel_block.d + (r.entry - a.sel_block.div(r.entry) * a.sel_block.d);
+        pos = pos < 0 ? -1 : pos * a.rec_tokens.d + sub;
+        blk = pos < 0 ? -1 : pos <= INT32_MAX ? a.S.div(static_cast<uint32_t>(pos)) : pos / a.S.d;
+      }
+      if (blk >= 0 && blk < a.scale_blocks) {
         if (pos >= seq) return k;
         if (r.slot >= 0 && r.slot <= a.B) {
           k.row = hot + r.slot * a.hot_row;
@@ -633,76 +836,74 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
         if (a.status) atomicOr(a.status, HISPARSE_ERR_RANGE);
         return k;
       }
-      k.row += sub * a.row_bytes;
-      const float *sc = scales + blk * a.columns;
-      k.k = sc[0];
-      k.v = sc[v_col];
+      if (!plain) k.row += sub * a.row_bytes;
+      k.scales = scales + blk * a.columns;
       return k;
     };
-    int issued = 0, signalled = 0;
-    Token cur = token(raw(0), 0);
-    Raw next = raw(1);
-    // A tile's rows, `per` of them this warp's: 16-byte chunks in passes of a power of two of
-    // columns, so that a lane's column, and with it all but the row, is fixed in a pass.
-    auto issue = [&]() {
-      const int i = issued, s = i % a.stages;
-      const int cn = min(a.tile, t1 - t0 - i * a.tile);
-      const Token ahead = token(next, i + 1);
-      next = raw(i + 2);
-      if (lane < per)
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(base + a.off_meta + (s * a.tile + pw * per + lane) * 8),
-                     "f"(cur.row ? cur.k : __int_as_float(0x7fffffff)), "f"(cur.v)
-                     : "memory");
-      const uint32_t have = __ballot_sync(0xffffffffu, cur.row != nullptr);
-      const uint64_t row = reinterpret_cast<uint64_t>(cur.row ? cur.row + k_at : a.hot);
-      const int rows = min(per, max(0, ((cn + 31) & ~31) - pw * per));
-      const uint32_t st = base + s * a.stage_bytes + pw * per * 128;
-      for (int col0 = 0; col0 < cpr;) {
-        const int left = cpr - col0, lw = left >= 32 ? 5 : 31 - __clz(left);
-        const int tl = lane >> lw, col = col0 + (lane & ((1 << lw) - 1));
-        const bool is_k = col < kc;
-        const int j = is_k ? col : col - kc;
-        const int64_t src_off = 16 * col + (is_k ? 0 : v_at);
-        const uint32_t dst_off = st + ((is_k ? 0 : a.k_chunks) + (j >> 3)) * a.tile * 128;
-#pragma unroll 4
-        for (int tb = 0; tb < rows; tb += 32 >> lw) {
-          const int t = tb + tl;
-          const uint64_t src = __shfl_sync(0xffffffffu, row, t & 31);
-          const bool ok = have >> (t & 31) & 1;
-          if (t < rows)
-            cp_async16(dst_off + t * 128 + ((j & 7 ^ (t & 7)) << 4),
-                       reinterpret_cast<const char *>(src) + (ok ? src_off : 0), ok ? 16 : 0);
-        }
-        col0 += 1 << lw;
-      }
-      cp_commit();
-      cur = ahead;
-      ++issued;
+    // A warp's tokens of a tile: kPer of every 32 * looks.  Loads are two tiles ahead of their
+    // use: of slots and positions, and of the scales after the addresses are out.
+    constexpr int kLooks = Shape<N>::looks, kPer = 4 / kLooks;
+    const int first = (warp - Shape<N>::look) * 32 + lane;
+    auto index = [&](int u) { return first + 32 * kLooks * u; };
+    struct Scales {
+      float k[kPer], v[kPer];
     };
-    auto signal = [&]() {
-      cp_wait(issued - signalled - 1);
-      fence_async();
-      bar_arrive(b_full + 8 * (signalled % a.stages));
-      ++signalled;
+    auto put_scales = [&](int i, const Scales &x) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u)
+        if (index(u) < a.tile)
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(base + a.off_meta + (i % kTables * a.tile + index(u)) * 8),
+                       "f"(x.k[u]), "f"(x.v[u])
+                       : "memory");
+      bar_arrive(b_meta + 8 * (i % kTables));
     };
-    while (issued < min(tiles, a.stages)) issue();
-    make_q(kSoft + pw);
-    while (signalled < tiles) {
-      bool go = false;
-      if (issued < tiles) {
-        const uint32_t bar = b_empty + 8 * (issued % a.stages), parity = (issued / a.stages - 1) & 1;
-        if (issued == signalled) bar_wait(bar, parity, fail);
-        go = issued == signalled || __all_sync(0xffffffffu, bar_test(bar, parity));
+    // One tile's turn; r and x are those of every other tile, so that nothing waits for a load
+    // of the turn before.
+    auto turn = [&](int i, Raw (&r)[kPer], Scales &x) {
+      const int at = t0 + i * a.tile, slot = i % kTables;
+      Token now[kPer];
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        now[u] = token(r[u], at + index(u));
+        r[u] = raw(index(u) < a.tile ? at + 2 * a.tile + index(u) : t1);
       }
-      if (go) {
-        issue();
-      } else {
-        signal();
+      if (i >= kTables) bar_wait(b_used + 8 * slot, (i / kTables - 1) & 1, fail);
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        if (index(u) >= a.tile) break;
+        const uint32_t to = base + a.off_rows + (slot * a.tile + index(u)) * 8;
+        const uint64_t row = reinterpret_cast<uint64_t>(now[u].row);
+        asm volatile("st.shared.b64 [%0], %1;" ::"r"(to), "l"(row ? row + k_at : zeros) : "memory");
+        if (!a.latent)
+          asm volatile("st.shared.b64 [%0], %1;" ::"r"(to + kTables * a.tile * 8), "l"(row ? row + v_at : zeros)
+                       : "memory");
       }
+      bar_arrive(b_tab + 8 * slot);
+      if (i > 1) put_scales(i - 2, x);
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        x.k[u] = now[u].row ? now[u].scales[0] : __int_as_float(0x7fffffff);
+        x.v[u] = now[u].row ? now[u].scales[v_col] : 0.f;
+      }
+    };
+    Raw r0[kPer], r1[kPer];
+    Scales x0 = {}, x1 = {};
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      r0[u] = raw(index(u) < a.tile ? t0 + index(u) : t1);
+      r1[u] = raw(index(u) < a.tile ? t0 + a.tile + index(u) : t1);
     }
+    for (int i = 0; i < tiles; i += 2) {
+      turn(i, r0, x0);
+      if (i + 1 < tiles) turn(i + 1, r1, x1);
+    }
+    if (tiles > 1 && tiles % 2 == 0) put_scales(tiles - 2, x0);
+    if (tiles > 0 && tiles % 2 == 0) put_scales(tiles - 1, x1);
+    if (tiles > 1 && tiles % 2 == 1) put_scales(tiles - 2, x1);
+    if (tiles > 0 && tiles % 2 == 1) put_scales(tiles - 1, x0);
   } else {
     // ---- products: the whole warp walks the loops, one lane issues -------------------
-    const uint32_t d_qk = mma_desc(N, false, false);
+    const uint32_t d_qk = mma_desc(kQ, false, false);
     const uint32_t d_pv = mma_desc(N, false, true), d_pv5 = mma_desc(N, true, true);
     const int k_steps = (a.k_dim + 31) >> 5;
     const uint32_t elected = elect_one();
@@ -710,33 +911,24 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
     bar_wait(b_q, 0, fail);
     auto scores = [&](int i) {
       const int s = i % a.stages;
-      bar_wait(b_full + 8 * s, (i / a.stages) & 1, fail);
-      __syncwarp();
-      tc_after();
-      const uint32_t d = tmem + (i & 1) * N;
-      uint32_t q = q_desc;
-      for (int t = 0; t < kTerms; ++t) {
-        uint32_t k = smem_desc(base + s * a.stage_bytes);
-        for (int left = k_steps; left > 0; left -= 4) {
+      const uint32_t d = tmem + (i & 1) * kQ;
+      uint32_t q = q_desc, k = smem_desc(base + s * a.stage_bytes);
+      int left = k_steps;
+      for (; left >= 4; left -= 4) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (e < left) mma_f8(d, k + 2 * e, q + 2 * e, d_qk, t > 0 || left < k_steps || e > 0, elected);
-          k += a.tile * 8;
-          q += N * 8;
-        }
+        for (int e = 0; e < 4; ++e) mma_f8(d, k + 2 * e, q + 2 * e, d_qk, e > 0 || left < k_steps, elected);
+        k += a.tile * 8;
+        q += kQ * 8;
       }
+      for (int e = 0; e < left; ++e) mma_f8(d, k + 2 * e, q + 2 * e, d_qk, e > 0 || left < k_steps, elected);
       tc_commit(b_s + 8 * (i & 1), elected);
     };
-    if (tiles > 0) scores(0);
-    for (int i = 0; i < tiles; ++i) {
-      if (i + 1 < tiles) scores(i + 1);
+    auto values = [&](int i) {
       const int s = i % a.stages, cn = min(a.tile, t1 - t0 - i * a.tile);
-      bar_wait(b_p, i & 1, fail);
-      __syncwarp();
-      tc_after();
       uint32_t v = smem_desc(base + s * a.stage_bytes + (a.latent ? 0 : a.k_chunks * a.tile * 128));
       const int steps = (cn + 31) >> 5;
       for (int j = 0; j < a.v_tiles; ++j) {
+#pragma unroll 4
         for (int k = 0; k < steps; ++k)
 #pragma unroll
           for (int t = 0; t < kTerms; ++t)
@@ -745,7 +937,32 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
         v += a.tile * 8;
       }
       tc_commit(b_empty + 8 * s, elected);
+      tc_commit(b_used + 8 * (i % kTables), elected);
       tc_commit(b_pv, elected);
+    };
+    // Whatever is ready first: the scores of the next tile (at most one ahead, for two score
+    // buffers) or the values of this one.
+    int qk = 0, pv = 0;
+    long long since = clock64();
+    while (pv < tiles) {
+      bool did = false;
+      if (qk < tiles && qk <= pv + 1 &&
+          __all_sync(0xffffffffu, bar_test(b_full + 8 * (qk % a.stages), (qk / a.stages) & 1) || *fail)) {
+        tc_after();
+        scores(qk++);
+        did = true;
+      }
+      if (qk > pv && __all_sync(0xffffffffu, bar_test(b_p, pv & 1) || *fail)) {
+        tc_after();
+        values(pv++);
+        did = true;
+      }
+      if (did) {
+        since = clock64();
+      } else if (clock64() - since > (1ll << 32)) {
+        *fail = 1;
+      }
+      __syncwarp();
     }
   }
   // ---- join ----------------------------------------------------------------------
@@ -778,9 +995,11 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const float f = s_f[c0 + c];
-          if (c0 + c < heads)
-            out[static_cast<int64_t>(h0 + c0 + c) * a.out_head + d] = from_f32<T>(f != 0.f ? o[c] * f : 0.f);
+          o[c] = f != 0.f ? o[c] * f : 0.f;
         }
+        T *p = reinterpret_cast<T *>(smem_raw + (base - smem_u32(smem_raw))) + c0 * a.v_dim + d;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) p[c * a.v_dim] = from_f32<T>(o[c]);
       } else {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -797,11 +1016,19 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
           z > 0.f || z != z ? (s_m[tid] + log2f(z)) * 0.6931471805599453f : -INFINITY;
     }
     __syncthreads();
+    const T *p = reinterpret_cast<const T *>(smem_raw + (base - smem_u32(smem_raw)));
+    const uint32_t total = heads * (a.quads.d >> 1);
+    for (uint32_t i = tid; i < total; i += kThreads) {
+      uint32_t n, d;
+      a.quads.divmod(2 * i, n, d);
+      *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(h0 + n) * a.out_head + 4 * d) =
+          *reinterpret_cast<const uint4 *>(p + n * a.v_dim + 4 * d);
+    }
   } else {
     __syncwarp();
     cluster_sync();
   }
-  if (warp == kWorkers) {
+  if (warp == Shape<N>::mma) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(a.tmem_cols));
   }
@@ -821,7 +1048,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, N == 16 ? 2 : 1) attend_ker
 #pragma unroll 4
     for (int r = 0; r < a.cluster; ++r) {
       const float x = s_w[r * N + tid], y = ld_peer(peer(smem_u32(&s_l[n]), r));
-      const float w = x > -INFINITY ? ex2(x - m) : 0.f;
+      const float w = ex2(x - m);
       s_w[r * N + tid] = w;
       z = fmaf(w, y, z);
     }
@@ -876,16 +1103,50 @@ bool plan_smem(AttendArgs &a, int N, int terms, int tile, uint32_t limit, uint32
   // rows beyond a tile that the 128-row products read stay inside: Q and P follow
   const uint32_t over = (128 - tile) * 128;
   const uint32_t rest = q + p + (q + p < over ? over - q - p : 0);
-  const uint32_t meta = tile * 8;
+  // tables: two scales a token, and an address (two with a V part)
+  const uint32_t meta = kTables * tile * (a.latent ? 16 : 24);
   const uint32_t sums = static_cast<uint32_t>(N) * a.v_dim * 4;
-  const uint32_t fixed = rest + 1024;
-  if (fixed + 2 * (a.stage_bytes + meta) > limit) return false;
-  a.stages = std::min<uint32_t>(kMaxStages, (limit - fixed) / (a.stage_bytes + meta));
+  const uint32_t fixed = rest + meta + 1024;
+  if (fixed + 2 * a.stage_bytes > limit) return false;
+  a.stages = std::min<uint32_t>(kMaxStages, (limit - fixed) / a.stage_bytes);
   a.off_q = a.stages * a.stage_bytes;
   a.off_p = a.off_q + q;
   a.off_meta = a.off_q + rest;
-  bytes = std::max(a.off_meta + a.stages * meta, sums) + 1024;
+  a.off_rows = a.off_meta + kTables * tile * 8;
+  bytes = std::max(a.off_meta + meta, sums) + 1024;
   return bytes <= limit;
+}
+
+// Clusters of c CTAs that the GPU runs at once (asked once for each of the few
+// combinations that a program uses).
+int active_clusters(const void *fn, int threads, uint32_t bytes, int c, int dev) {
+  struct Known {
+    const void *fn;
+    uint32_t bytes;
+    int c, dev, n;
+  };
+  thread_local Known known[64];
+  thread_local int count = 0;
+  for (int i = 0; i < std::min(count, 64); ++i)
+    if (known[i].fn == fn && known[i].bytes == bytes && known[i].c == c && known[i].dev == dev) return known[i].n;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(c);
+  lc.blockDim = dim3(threads);
+  lc.dynamicSmemBytes = bytes;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = c;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &lc) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  known[count++ % 64] = {fn, bytes, c, dev, n};
+  return n;
 }
 
 template <class T, int N>
@@ -893,7 +1154,7 @@ int launch_attend(AttendArgs a, int64_t units, void *stream) {
   // TMEM: two score buffers and the sums, a power of two of columns.
   int cols = 32;
   a.v_tiles = (a.v_dim + 127) / 128;
-  while (cols < 2 * N + a.v_tiles * N) cols *= 2;
+  while (cols < 2 * Terms<T>::n * N + a.v_tiles * N) cols *= 2;
   a.tmem_cols = cols;
   const int64_t tokens = static_cast<int64_t>(a.entries) * a.rec_tokens.d;
   auto fn = attend_kernel<T, N>;
@@ -907,6 +1168,8 @@ int launch_attend(AttendArgs a, int64_t units, void *stream) {
     fixed.store(static_cast<uint32_t>(fa.sharedSizeBytes));
     HS_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSmemCta - static_cast<uint32_t>(fa.sharedSizeBytes)));
+    HS_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared));
     HS_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     ready.fetch_or(1ull << (dev & 63));
   }
@@ -917,16 +1180,15 @@ int launch_attend(AttendArgs a, int64_t units, void *stream) {
   const uint32_t least = std::min(whole, kSmemSm / 512 * cols - 1024);
   uint32_t bytes = 0;
   bool ok = false;
-  const uint32_t limits[2] = {std::max(least, kSmemSm / 2 - 1024 - fixed.load()), whole};
-  for (int l = N == 16 ? 0 : 1; l < 2 && !ok; ++l)
-    for (int tile = 128; tile >= 64 && !ok; tile -= 32)
-      ok = plan_smem(a, N, Terms<T>::n, tile, limits[l], bytes);
+  for (int tile = 128; tile >= 64 && !ok; tile -= 32) ok = plan_smem(a, N, Terms<T>::n, tile, whole, bytes);
   if (!ok) return HISPARSE_EBOUND;
   bytes = std::max(bytes, least);
-  const int per_sm = 2 * (bytes + fixed.load() + 1024) <= kSmemSm ? 2 : 1;
-  // Split the tokens while there are SMs without work and a CTA keeps 64 tokens or more.
+  // Split the tokens over a cluster while all clusters still run at once and a CTA keeps 64
+  // tokens or more.
   int c = 1;
-  while (c < kMaxCluster && units * c * 2 <= 152 * per_sm && tokens >= static_cast<int64_t>(c) * 2 * 64) c *= 2;
+  while (c < kMaxCluster && tokens >= static_cast<int64_t>(c) * 2 * 64 &&
+         units <= active_clusters(reinterpret_cast<const void *>(fn), Shape<N>::threads, bytes, 2 * c, dev))
+    c *= 2;
   a.cluster = c;
   a.per_cta = static_cast<int>(((tokens + c - 1) / c + 31) / 32 * 32);
   if (units * c > 0x7fffffff) return HISPARSE_EBOUND;
