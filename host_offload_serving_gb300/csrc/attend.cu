@@ -21,7 +21,7 @@
 // Warps: four softmax warps (a lane a token, TMEM lane = token) for each 32 columns; six or
 // eight that gather (16-byte cp.async into the 128-byte-swizzled tiles that the tensor cores
 // read, several tiles ahead); one or two that turn slots and positions into addresses and scales;
-// and one that issues the products.  S is double buffered in TMEM, so the scores of tile i+1
+// and two that issue the products.  S is double buffered in TMEM, so the scores of tile i+1
 // are computed while the softmax of tile i runs.  O is rescaled only where a column's
 // maximum has grown by more than 2^2.75 since it was last set.
 #include <algorithm>
@@ -32,7 +32,6 @@
 
 namespace {
 
-constexpr int kTables = 4;  // tiles whose rows' addresses and scales are known ahead
 constexpr int kMaxStages = 6;
 constexpr int kMaxCluster = 16;
 constexpr float kNone = -1e30f; // a CTA's offset where it had no token
@@ -52,15 +51,14 @@ struct AttendArgs {
   float *lse;
   const int32_t *sel, *slots;
   const char *hot;
-  int64_t hot_req, hot_row;
+  int64_t hot_req;
+  uint32_t hot_row, res_row, res_rows, row_bytes;  // row_bytes: a token's part of a record
   const char *resident;
-  int64_t res_rows, res_row;
   const float *scales;
   int64_t scales_req;
-  int32_t scale_blocks;
+  uint32_t scale_blocks;
   const int32_t *seq_lens, *num_reqs;
   uint32_t *status;
-  int64_t row_bytes;  // a token's part of a record
   // the launch's plan
   int32_t cluster, per_cta, tile, stages, k_chunks, v_chunks, v_tiles, tmem_cols;
   FastDiv quads;  // v_dim / 4
@@ -77,22 +75,11 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {  // never suspends
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {  // suspended for up to 100 us
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p;\n"
-      " mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+      " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, 100000;\n"
       " selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -103,18 +90,14 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // *fail, after which no wait of the CTA waits any more: every loop still makes
 // its turns, so barriers stay matched, TMEM is freed and the kernel ends, with
 // HISPARSE_ERR_WAIT in the status.
-__device__ __noinline__ void bar_wait_slow(uint32_t bar, uint32_t parity, volatile int *fail) {
+__device__ __noinline__ void bar_wait_long(uint32_t bar, uint32_t parity, volatile int *fail) {
   const long long start = clock64();
-  while (clock64() - start < (1ll << 32)) {
-    if (bar_try(bar, parity) || *fail) return;
+  while (!bar_try(bar, parity) && !*fail) {
+    if (clock64() - start > (1ll << 32)) *fail = 1;
   }
-  *fail = 1;
 }
 __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile int *fail) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (bar_try(bar, parity)) return;
-  bar_wait_slow(bar, parity, fail);
+  if (!bar_try(bar, parity)) bar_wait_long(bar, parity, fail);
 }
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -131,13 +114,10 @@ __device__ __forceinline__ uint32_t elect_one() {
       "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r)::"memory");
   return r;
 }
-// The elected lane's mbarrier arrival once its products so far are done.
-__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t elected) {
-  asm volatile(
-      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
-      "r"(elected)
-      : "memory");
+// This lane's mbarrier arrival once its products so far are done.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
 }
 // Shared-memory descriptor of a 128-byte-swizzled operand whose groups of 8 rows are 1024
 // bytes apart (either major-ness: the other offset is not used).  Its lower word; the
@@ -149,14 +129,16 @@ __device__ __forceinline__ uint32_t mma_desc(int n, bool b_e5m2, bool transposed
   return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (transposed ? 3u << 15 : 0u) |
          (static_cast<uint32_t>(n) >> 3 << 17) | (128u >> 4 << 24);
 }
-__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
-                                       uint32_t accumulate, uint32_t elected) {
+// Products are issued by one lane, in unrolled runs of constant offsets: the operands go through
+// uniform registers, and a run of any length keeps the tensor cores fed (39 cycles an
+// instruction for 16 columns, 64 for 128), where a loop around one took 100.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b64 da, db;\n"
-      " setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
-      " mov.b64 da, {%1, %6};\n mov.b64 db, {%2, %6};\n"
-      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(elected), "r"(kDescHi)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n"
+      " setp.ne.b32 p, %4, 0;\n"
+      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t *r) {
@@ -194,16 +176,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, uint64_t src) {
 }
 // What a masked token's row reads: zeros, as its probability is 0 and 0 * NaN is not.
 __device__ uint4 g_zeros[640 / 16];
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait(int pending) {
-  switch (pending) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-  }
+// Arrives once this thread's copies so far are complete.  Their bytes are then seen by whoever
+// waited for the barrier, and by that thread's tensor-core reads after its proxy fence.
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ float warp_max(float x) {
   float r;
@@ -320,9 +296,17 @@ __device__ __forceinline__ float abs_max<__half>(const uint4 (&v)[3]) {
   return fmaxf(__low2float(m), __high2float(m));
 }
 // 8 values times `up` as e4m3 terms; word 0 holds the terms of the first four.
+// (Out of line: unrolled into its callers it would be a sixth of the kernel, which does not fit the
+// instruction cache as it is.)
+template <int kTerms>
+struct Split {
+  uint32_t w0[kTerms], w1[kTerms];
+};
 template <class T, int kTerms>
-__device__ __forceinline__ void split8(const uint4 &v, float up, uint32_t (&w0)[kTerms], uint32_t (&w1)[kTerms]) {
+__device__ __noinline__ Split<kTerms> split8(uint4 v, float up) {
   const T *e = reinterpret_cast<const T *>(&v);
+  Split<kTerms> s;
+  uint32_t (&w0)[kTerms] = s.w0, (&w1)[kTerms] = s.w1;
   if constexpr (kTerms == 2) {
     // |x| < 256: in f16, 11 significant bits against the 8 of the values, and as far down as
     // the second term reaches.
@@ -356,6 +340,7 @@ __device__ __forceinline__ void split8(const uint4 &v, float up, uint32_t (&w0)[
       w1[t] |= take_term<false>(x[6], x[7]) << 16;
     }
   }
+  return s;
 }
 
 // 2^kLw columns of 16-byte chunks of a warp's share of the rows: lane t * 2^kLw + c copies
@@ -385,12 +370,33 @@ __device__ __forceinline__ void gather_columns(uint32_t table, uint32_t off, uin
   }
 }
 
+// A tile's columns come, are multiplied and go in two halves: the chunks of K and of V, or those
+// of a latent record in two.  Chunks [c0, c1) of K or V; the values read [v0, v1) of them.
+struct Half {
+  int c0, c1, v0, v1;
+  bool is_v, scores;
+};
+__device__ __forceinline__ Half half_of(const AttendArgs &a, int u) {
+  if (!a.latent) return {0, u ? a.v_chunks : a.k_chunks, 0, u ? a.v_chunks : 0, u == 1, u == 0};
+  const int mid = (a.k_chunks + 1) >> 1, c0 = u ? mid : 0, c1 = u ? a.k_chunks : mid;
+  return {c0, c1, min(c0, a.v_tiles), min(c1, a.v_tiles), false, true};
+}
+
 // ---- tokens ------------------------------------------------------------------
+// A load, or a constant without one; nothing waits here for the load.
+__device__ __forceinline__ int32_t ld_if(const int32_t *p, bool take, int32_t other) {
+  int32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %2, 0;\n mov.b32 %0, %3;\n @p ld.global.b32 %0, [%1];\n}"
+      : "=&r"(r)
+      : "l"(p), "r"(static_cast<int>(take)), "r"(other));
+  return r;
+}
 struct Raw {
   int32_t slot, sel, entry;
 };
 struct Token {
-  const char *row;  // NULL: nothing to read
+  uint64_t row;  // address; 0: nothing to read
   const float *scales;
 };
 
@@ -432,10 +438,11 @@ struct Shape {
   static constexpr int groups = N > 32 ? N / 32 : 1;  // of four softmax warps
   static constexpr int cols = N / groups;             // columns of a softmax thread
   static constexpr int soft = 4 * groups;             // softmax warps
-  static constexpr int gather = N > 32 ? 6 : 8;       // warps that copy rows
-  static constexpr int mma = soft + gather;           // the warp that issues products
-  static constexpr int look = mma + 1;                // warps that look the rows up
-  static constexpr int looks = N > 32 ? 1 : 2;
+  static constexpr int gather = N > 32 ? 4 : 6;       // warps that copy rows
+  static constexpr int mma = soft + gather;           // two warps that issue products: scores, values
+  static constexpr int look = mma + 2;                // warps that look rows up
+  static constexpr int looks = N > 32 ? 2 : 4;
+  static constexpr int tables = N > 32 ? 4 : 8;      // tiles that are looked up ahead
   static constexpr int threads = 32 * (look + looks);
 };
 
@@ -443,20 +450,22 @@ template <class T, int N>
 __global__ void __launch_bounds__(Shape<N>::threads, 1)
     attend_kernel(const AttendArgs a) {
   constexpr int kTerms = Terms<T>::n;
-  constexpr int NC = Shape<N>::cols, kSoft = Shape<N>::soft, kGather = Shape<N>::gather;
+  constexpr int NC = Shape<N>::cols, kSoft = Shape<N>::soft, kGather = Shape<N>::gather, kTables = Shape<N>::tables;
   constexpr int kThreads = Shape<N>::threads;
   constexpr int kQ = kTerms * N;  // rows of Q: the terms of a head are N rows apart
   extern __shared__ char smem_raw[];
-  __shared__ uint64_t s_bars[2 * kMaxStages + 3 * kTables + 5];
+  __shared__ uint64_t s_bars[4 * kMaxStages + 3 * kTables + 7];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   __shared__ float s_l[N], s_f[N], s_d[N], s_wmax[4][N], s_w[kMaxCluster * N];
   __shared__ __align__(16) float s_qf[N], s_m[N];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = smem_u32(s_bars);
-  const uint32_t b_full = bars, b_empty = bars + 8 * kMaxStages, b_s = bars + 16 * kMaxStages;
+  const uint32_t b_full = bars, b_empty = bars + 16 * kMaxStages;  // [stage][half]
+  const uint32_t b_s = bars + 32 * kMaxStages;
   const uint32_t b_p = b_s + 16, b_pv = b_s + 24, b_q = b_s + 32;
-  const uint32_t b_tab = b_s + 40, b_meta = b_tab + 8 * kTables,
+  const uint32_t b_read = b_s + 40;  // a score buffer has been read
+  const uint32_t b_tab = b_s + 56, b_meta = b_tab + 8 * kTables,
                  b_used = b_meta + 8 * kTables;  // addresses and scales: written; done with
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = a.cluster > 1 ? blockIdx.x % a.cluster : 0;
@@ -466,12 +475,10 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
   const int req = static_cast<int>(qrow / a.rows);
 
   if (tid == 0) {
-    for (int s = 0; s < a.stages; ++s) {
-      bar_init(b_full + 8 * s, 32 * kGather);
-      bar_init(b_empty + 8 * s, 1);
-    }
     bar_init(b_s, 1);
     bar_init(b_s + 8, 1);
+    bar_init(b_read, 32 * kSoft);
+    bar_init(b_read + 8, 32 * kSoft);
     bar_init(b_p, 32 * kSoft);
     bar_init(b_pv, 1);
     bar_init(b_q, 32 * (kSoft + kGather));
@@ -481,11 +488,14 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       bar_init(b_used + 8 * t, 1);
     }
     s_fail = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  for (int i = tid; i < 2 * a.stages; i += kThreads) {
+    bar_init(b_full + 8 * i, 32 * kGather);
+    bar_init(b_empty + 8 * i, 1);
   }
   for (int c = tid; c < N; c += kThreads) s_m[c] = 0.f;
   // The last 16 of 32 K columns that a product reads beyond k_dim: zero in every
-  // stage (the gather never writes them) and in Q.
+  // stage (the copies never write them) and in Q.
   if (a.k_dim & 16) {
     const int c = a.k_dim >> 7, j = (a.k_dim & 127) >> 4;
     for (int i = tid; i < a.stages * a.tile; i += kThreads) {
@@ -497,6 +507,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     }
     fence_async();
   }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   pdl_wait();
   if (a.num_reqs && req >= *a.num_reqs) return;  // the whole cluster
   if (warp == Shape<N>::mma) {
@@ -553,11 +564,10 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
           if (lane + 32 * i >= vecs) continue;
           const int d = (lane + 32 * i) * 8;
           const uint32_t at = base + a.off_q + ((d >> 7) * kQ + n) * 128 + (((d & 127) >> 4 ^ (n & 7)) << 4) + (d & 15);
-          uint32_t w0[kTerms], w1[kTerms];
-          split8<T>(v[b][i], up, w0, w1);
+          const Split<kTerms> w = split8<T, kTerms>(v[b][i], up);
 #pragma unroll
           for (int t = 0; t < kTerms; ++t)
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + t * N * 128), "r"(w0[t]), "r"(w1[t])
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + t * N * 128), "r"(w.w0[t]), "r"(w.w1[t])
                          : "memory");
         }
       }
@@ -566,9 +576,10 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     bar_arrive(b_q);
   };
 
+  if (warp < Shape<N>::mma) make_q(warp);
+
   if (warp < kSoft) {
     // ---- softmax ---------------------------------------------------------------
-    make_q(warp);
     bar_wait(b_q, 0, fail);  // the factors of all heads
     const int grp = warp >> 2, wl = warp & 3, c0 = grp * NC, gt = tid & 127;
     float l[NC];
@@ -617,6 +628,8 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
           }
         }
       }
+      tc_before();
+      bar_arrive(b_read + 8 * (i & 1));
       // scores in powers of two, the V scale in them, above their column's offset
       float most = -INFINITY;
 #pragma unroll
@@ -731,23 +744,28 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     __syncwarp();
   } else if (warp < Shape<N>::mma) {
     // ---- gather ------------------------------------------------------------------
-    // Groups of 8 rows in turn, 16-byte chunks of them in passes of a power of two of columns.
+    // A tile comes in halves, each as soon as its place is free and with its own arrival.
     const int gw = warp - kSoft;
-    const int kc = a.k_dim >> 4, vc = a.latent ? 0 : a.v_dim >> 4;
-    make_q(warp);
-    int issued = 0, signalled = 0;
-    auto issue = [&]() {
-      const int i = issued, s = i % a.stages;
-      const int groups = (min(a.tile, t1 - t0 - i * a.tile) + 31) >> 5 << 2;
+    int s = 0, turn = 0;  // the tile's stage, and how often the stages went round
+    for (int i = 0; i < tiles; ++i) {
+      const int groups = (min(a.tile, t1 - t0 - i * a.tile) + 31) >> 5 << 2;  // of 8 rows
       const uint32_t st = base + s * a.stage_bytes;
       const uint32_t table = base + a.off_rows + i % kTables * a.tile * 8;
-      for (int part = 0; part < (vc ? 2 : 1); ++part) {
-        const int cols = part ? vc : kc;
-        const uint32_t rows = table + part * kTables * a.tile * 8;
-        for (int col0 = 0; col0 < cols;) {
+      bar_wait(b_tab + 8 * (i % kTables), (i / kTables) & 1, fail);
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) {
+        const Half half = half_of(a, u);
+        const uint32_t full = b_full + 16 * s + 8 * u;
+        const uint32_t to = st + (half.is_v ? a.k_chunks * a.tile * 128 : 0);
+        if (turn > 0) bar_wait(b_empty + 16 * s + 8 * u, (turn - 1) & 1, fail);
+        __syncwarp();
+        // 16-byte copies; of the groups of 8 rows a warp takes every kGather-th.
+        const int cols = min(8 * half.c1, (half.is_v ? a.v_dim : a.k_dim) >> 4);
+        const uint32_t rows = table + (half.is_v ? kTables * a.tile * 8 : 0);
+        for (int col0 = 8 * half.c0; col0 < cols;) {
           const int left = cols - col0, lw = left >= 32 ? 5 : 31 - __clz(left);
           const int j = col0 + (lane & ((1 << lw) - 1));
-          const uint32_t dst = st + ((part ? a.k_chunks : 0) + (j >> 3)) * a.tile * 128 + ((j & 7) << 4);
+          const uint32_t dst = to + (j >> 3) * a.tile * 128 + ((j & 7) << 4);
           switch (lw) {
             case 5: gather_columns<5, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
             case 4: gather_columns<4, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
@@ -758,211 +776,206 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
           }
           col0 += 1 << lw;
         }
+        cp_arrive(full);
       }
-      cp_commit();
-      ++issued;
-    };
-    auto signal = [&]() {
-      cp_wait(issued - signalled - 1);
-      fence_async();
-      bar_arrive(b_full + 8 * (signalled % a.stages));
-      ++signalled;
-    };
-    while (signalled < tiles) {
-      bool go = false;
-      if (issued < tiles) {
-        // the stage is free and the rows are known; with nothing in flight, wait for both
-        const bool fresh = issued < a.stages;
-        const uint32_t free = b_empty + 8 * (issued % a.stages), fp = (issued / a.stages - 1) & 1;
-        const uint32_t known = b_tab + 8 * (issued % kTables), kp = (issued / kTables) & 1;
-        go = issued == signalled;
-        if (go) {
-          if (!fresh) bar_wait(free, fp, fail);
-          bar_wait(known, kp, fail);
-        } else {
-          go = __all_sync(0xffffffffu, (fresh || bar_test(free, fp)) && bar_test(known, kp));
-        }
-        __syncwarp();
-      }
-      if (go) {
-        issue();
-      } else {
-        signal();
-      }
+      if (++s == a.stages) s = 0, ++turn;
     }
   } else if (warp >= Shape<N>::look) {
     // ---- rows: slot -> address, position -> scales, tiles ahead of their copies --------
-    const int64_t k_at = static_cast<int64_t>(kvh) * a.k_dim;
-    const int64_t v_at = static_cast<int64_t>(a.kv_heads) * a.k_dim + static_cast<int64_t>(kvh) * a.v_dim;
-    const int seq = a.seq_lens ? a.seq_lens[req] : INT32_MAX;
+    const uint32_t k_at = kvh * a.k_dim, v_at = a.kv_heads * a.k_dim + kvh * a.v_dim;
+    const uint32_t seq = a.seq_lens ? max(0, a.seq_lens[req]) : 0x80000000u;
     const float *scales = a.scales + req * a.scales_req + kvh;
     const char *hot = a.hot + req * a.hot_req;
     const int v_col = a.latent ? 0 : a.kv_heads;
-    const int64_t sel0 = entry0 / a.sel_block.d;
+    const int32_t *slots = a.slots + entry0, *sels = a.sel + entry0 / a.sel_block.d;
     const uint64_t zeros = reinterpret_cast<uint64_t>(g_zeros);
     const bool plain = a.rec_tokens.d == 1 && a.sel_block.d == 1;  // an entry is a token
     auto raw = [&](int t) {
-      Raw r = {-1, -1, t};
-      if (t < t1) {
-        if (!plain) r.entry = static_cast<int>(a.rec_tokens.div(t));
-        r.slot = a.slots[entry0 + r.entry];
-        r.sel = a.sel[plain ? entry0 + t : sel0 + a.sel_block.div(r.entry)];
-      }
+      Raw r;
+      r.entry = plain ? t : static_cast<int>(a.rec_tokens.div(t));
+      r.slot = ld_if(slots + r.entry, t < t1, -1);
+      r.sel = ld_if(sels + (plain ? t : static_cast<int>(a.sel_block.div(r.entry))), t < t1, -1);
       return r;
     };
     auto token = [&](const Raw &r, int t) {
-      Token k = {nullptr, nullptr};
-      if (r.slot == -1) return k;
-      int64_t pos = r.sel, blk;
-      int sub = 0;
-      if (plain) {
-        blk = pos < 0 ? -1 : static_cast<int64_t>(a.S.div(r.sel));
-      } else {
-        sub = t - r.entry * static_cast<int>(a.rec_tokens.d);
-        if (a.sel_block.d > 1 && pos >= 0)
-          pos = pos * a.sel_block.d + (r.entry - a.sel_block.div(r.entry) * a.sel_block.d);
-        pos = pos < 0 ? -1 : pos * a.rec_tokens.d + sub;
-        blk = pos < 0 ? -1 : pos <= INT32_MAX ? a.S.div(static_cast<uint32_t>(pos)) : pos / a.S.d;
+      Token k = {0, nullptr};
+      uint32_t pos = r.sel, sub = 0;  // a position past 2^31 - 1 (one below 0) is in no block
+      if (!plain) {
+        const uint32_t block = a.sel_block.div(r.entry);
+        sub = t - r.entry * a.rec_tokens.d;
+        const int64_t rec = static_cast<int64_t>(r.sel) * a.sel_block.d + (r.entry - block * a.sel_block.d);
+        const int64_t p = rec * a.rec_tokens.d + sub;  // (below 2^63: sel_block and rec_tokens are below 2^16)
+        pos = r.sel < 0 || p > INT32_MAX ? 0x80000000u : static_cast<uint32_t>(p);
       }
-      if (blk >= 0 && blk < a.scale_blocks) {
-        if (pos >= seq) return k;
-        if (r.slot >= 0 && r.slot <= a.B) {
-          k.row = hot + r.slot * a.hot_row;
-        } else if (r.slot > a.B && r.slot - a.B - 1 < a.res_rows) {
-          k.row = a.resident + (static_cast<int64_t>(r.slot) - a.B - 1) * a.res_row;
+      const uint32_t blk = a.S.div(pos & 0x7fffffffu), near = r.slot, far = r.slot - a.B - 1;
+      const bool is_near = near <= static_cast<uint32_t>(a.B), is_far = r.slot > a.B && far < a.res_rows;
+      const bool inside = pos < 0x80000000u && blk < a.scale_blocks;
+      if (r.slot != -1) {
+        if (inside && pos < seq && (is_near || is_far)) {
+          const uint64_t base0 = reinterpret_cast<uint64_t>(is_near ? hot : a.resident);
+          k.row = base0 + static_cast<uint64_t>(is_near ? near : far) * (is_near ? a.hot_row : a.res_row);
+          if (!plain) k.row += static_cast<uint64_t>(sub) * a.row_bytes;
+          k.scales = scales + blk * a.columns;
+        } else if (a.status && !(inside && pos >= seq)) {
+          atomicOr(a.status, HISPARSE_ERR_RANGE);
         }
       }
-      if (!k.row) {
-        if (a.status) atomicOr(a.status, HISPARSE_ERR_RANGE);
-        return k;
-      }
-      if (!plain) k.row += sub * a.row_bytes;
-      k.scales = scales + blk * a.columns;
       return k;
     };
-    // A warp's tokens of a tile: kPer of every 32 * looks.  Loads are two tiles ahead of their
-    // use: of slots and positions, and of the scales after the addresses are out.
-    constexpr int kLooks = Shape<N>::looks, kPer = 4 / kLooks;
-    const int first = (warp - Shape<N>::look) * 32 + lane;
-    auto index = [&](int u) { return first + 32 * kLooks * u; };
-    struct Scales {
-      float k[kPer], v[kPer];
+    // In steps of a token a lane, `per` of them a tile.  Loads are kAhead steps ahead of their
+    // use: of slots and positions, and of the scales after the addresses are out; each of kAhead
+    // steps in turn has its own registers, so that none waits for another's load.
+    constexpr int kLooks = Shape<N>::looks, kAhead = 4;
+    const int per = (a.tile + 32 * kLooks - 1) / (32 * kLooks), steps = tiles * per;
+    const int mine = (warp - Shape<N>::look) * 32 + lane;
+    struct Step {
+      Raw r;
+      int32_t k, v;
     };
-    auto put_scales = [&](int i, const Scales &x) {
-#pragma unroll
-      for (int u = 0; u < kPer; ++u)
-        if (index(u) < a.tile)
-          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(base + a.off_meta + (i % kTables * a.tile + index(u)) * 8),
-                       "f"(x.k[u]), "f"(x.v[u])
-                       : "memory");
-      bar_arrive(b_meta + 8 * (i % kTables));
+    auto fetch = [&](Step &x, int tile, int sub) {
+      const int j = mine + 32 * kLooks * sub;
+      x.r = raw(j < a.tile ? t0 + tile * a.tile + j : t1);
     };
-    // One tile's turn; r and x are those of every other tile, so that nothing waits for a load
-    // of the turn before.
-    auto turn = [&](int i, Raw (&r)[kPer], Scales &x) {
-      const int at = t0 + i * a.tile, slot = i % kTables;
-      Token now[kPer];
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        now[u] = token(r[u], at + index(u));
-        r[u] = raw(index(u) < a.tile ? at + 2 * a.tile + index(u) : t1);
+    auto put_scales = [&](const Step &x, int tile, int sub) {
+      const int j = mine + 32 * kLooks * sub;
+      if (j < a.tile)
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(base + a.off_meta + (tile % kTables * a.tile + j) * 8),
+                     "r"(x.k), "r"(x.v)
+                     : "memory");
+      if (sub == per - 1) bar_arrive(b_meta + 8 * (tile % kTables));
+    };
+    // Steps kAhead behind, now, and kAhead ahead: (tile, sub) of each.
+    int bt = 0, bs = 0, nt = 0, ns = 0, at = 0, as = 0;
+    auto advance = [&](int &tile, int &sub) {
+      if (++sub == per) {
+        sub = 0;
+        ++tile;
       }
-      if (i >= kTables) bar_wait(b_used + 8 * slot, (i / kTables - 1) & 1, fail);
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        if (index(u) >= a.tile) break;
-        const uint32_t to = base + a.off_rows + (slot * a.tile + index(u)) * 8;
-        const uint64_t row = reinterpret_cast<uint64_t>(now[u].row);
-        asm volatile("st.shared.b64 [%0], %1;" ::"r"(to), "l"(row ? row + k_at : zeros) : "memory");
+    };
+    auto step = [&](Step &x, int n) {
+      if (n >= steps) return;
+      const int slot = nt % kTables, j = mine + 32 * kLooks * ns;
+      const Token now = token(x.r, t0 + nt * a.tile + j);
+      fetch(x, at, as);
+      advance(at, as);
+      if (ns == 0 && nt >= kTables) bar_wait(b_used + 8 * slot, (nt / kTables - 1) & 1, fail);
+      if (j < a.tile) {
+        const uint32_t to = base + a.off_rows + (slot * a.tile + j) * 8;
+        asm volatile("st.shared.b64 [%0], %1;" ::"r"(to), "l"(now.row ? now.row + k_at : zeros) : "memory");
         if (!a.latent)
-          asm volatile("st.shared.b64 [%0], %1;" ::"r"(to + kTables * a.tile * 8), "l"(row ? row + v_at : zeros)
+          asm volatile("st.shared.b64 [%0], %1;" ::"r"(to + kTables * a.tile * 8), "l"(now.row ? now.row + v_at : zeros)
                        : "memory");
       }
-      bar_arrive(b_tab + 8 * slot);
-      if (i > 1) put_scales(i - 2, x);
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        x.k[u] = now[u].row ? now[u].scales[0] : __int_as_float(0x7fffffff);
-        x.v[u] = now[u].row ? now[u].scales[v_col] : 0.f;
+      if (ns == per - 1) bar_arrive(b_tab + 8 * slot);
+      advance(nt, ns);
+      if (n >= kAhead) {
+        put_scales(x, bt, bs);
+        advance(bt, bs);
       }
+      const int32_t *sc = reinterpret_cast<const int32_t *>(now.scales);
+      x.k = ld_if(sc, now.row != 0, 0x7fffffff);
+      x.v = ld_if(sc + v_col, now.row != 0, 0);
     };
-    Raw r0[kPer], r1[kPer];
-    Scales x0 = {}, x1 = {};
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      r0[u] = raw(index(u) < a.tile ? t0 + index(u) : t1);
-      r1[u] = raw(index(u) < a.tile ? t0 + a.tile + index(u) : t1);
+    Step x0, x1, x2, x3;
+    fetch(x0, at, as), advance(at, as);
+    fetch(x1, at, as), advance(at, as);
+    fetch(x2, at, as), advance(at, as);
+    fetch(x3, at, as), advance(at, as);
+#pragma unroll 1
+    for (int n = 0; n < steps; n += kAhead) {
+      step(x0, n);
+      step(x1, n + 1);
+      step(x2, n + 2);
+      step(x3, n + 3);
     }
-    for (int i = 0; i < tiles; i += 2) {
-      turn(i, r0, x0);
-      if (i + 1 < tiles) turn(i + 1, r1, x1);
+    // the last kAhead steps' scales, in order
+#pragma unroll 1
+    for (int n = max(0, steps - kAhead); n < steps; ++n) {
+      const int w = n & 3;
+      const Step x = w == 0 ? x0 : w == 1 ? x1 : w == 2 ? x2 : x3;
+      put_scales(x, bt, bs);
+      advance(bt, bs);
     }
-    if (tiles > 1 && tiles % 2 == 0) put_scales(tiles - 2, x0);
-    if (tiles > 0 && tiles % 2 == 0) put_scales(tiles - 1, x1);
-    if (tiles > 1 && tiles % 2 == 1) put_scales(tiles - 2, x1);
-    if (tiles > 0 && tiles % 2 == 1) put_scales(tiles - 1, x0);
   } else {
-    // ---- products: the whole warp walks the loops, one lane issues -------------------
+    // ---- products: a warp for the scores and one for the values; one lane issues -----------
     const uint32_t d_qk = mma_desc(kQ, false, false);
     const uint32_t d_pv = mma_desc(N, false, true), d_pv5 = mma_desc(N, true, true);
     const int k_steps = (a.k_dim + 31) >> 5;
-    const uint32_t elected = elect_one();
+    const bool elected = elect_one();
     const uint32_t q_desc = smem_desc(base + a.off_q), p_desc = smem_desc(base + a.off_p);
-    bar_wait(b_q, 0, fail);
-    auto scores = [&](int i) {
-      const int s = i % a.stages;
+    // A half's part of tile i's scores.
+    int s = 0, turn = 0;  // the tile's stage, and how often the stages went round
+    auto scores = [&](int i, int u) {
+      const Half half = half_of(a, u);
       const uint32_t d = tmem + (i & 1) * kQ;
-      uint32_t q = q_desc, k = smem_desc(base + s * a.stage_bytes);
-      int left = k_steps;
-      for (; left >= 4; left -= 4) {
+      uint32_t q = q_desc + half.c0 * kQ * 8, k = smem_desc(base + s * a.stage_bytes) + half.c0 * a.tile * 8;
+      if (elected) {
+        int left = k_steps - 4 * half.c0;
+        for (int c = half.c0; c < half.c1; ++c, left -= 4, k += a.tile * 8, q += kQ * 8) {
+          if (left >= 4) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mma_f8(d, k + 2 * e, q + 2 * e, d_qk, e > 0 || left < k_steps, elected);
-        k += a.tile * 8;
-        q += kQ * 8;
-      }
-      for (int e = 0; e < left; ++e) mma_f8(d, k + 2 * e, q + 2 * e, d_qk, e > 0 || left < k_steps, elected);
-      tc_commit(b_s + 8 * (i & 1), elected);
-    };
-    auto values = [&](int i) {
-      const int s = i % a.stages, cn = min(a.tile, t1 - t0 - i * a.tile);
-      uint32_t v = smem_desc(base + s * a.stage_bytes + (a.latent ? 0 : a.k_chunks * a.tile * 128));
-      const int steps = (cn + 31) >> 5;
-      for (int j = 0; j < a.v_tiles; ++j) {
-#pragma unroll 4
-        for (int k = 0; k < steps; ++k)
-#pragma unroll
-          for (int t = 0; t < kTerms; ++t)
-            mma_f8(t_o + j * N, v + k * 256, p_desc + k * 256 + t * N / 16,
-                   t + 1 < kTerms ? d_pv : d_pv5, i > 0 || k > 0 || t > 0, elected);
-        v += a.tile * 8;
-      }
-      tc_commit(b_empty + 8 * s, elected);
-      tc_commit(b_used + 8 * (i % kTables), elected);
-      tc_commit(b_pv, elected);
-    };
-    // Whatever is ready first: the scores of the next tile (at most one ahead, for two score
-    // buffers) or the values of this one.
-    int qk = 0, pv = 0;
-    long long since = clock64();
-    while (pv < tiles) {
-      bool did = false;
-      if (qk < tiles && qk <= pv + 1 &&
-          __all_sync(0xffffffffu, bar_test(b_full + 8 * (qk % a.stages), (qk / a.stages) & 1) || *fail)) {
-        tc_after();
-        scores(qk++);
-        did = true;
-      }
-      if (qk > pv && __all_sync(0xffffffffu, bar_test(b_p, pv & 1) || *fail)) {
-        tc_after();
-        values(pv++);
-        did = true;
-      }
-      if (did) {
-        since = clock64();
-      } else if (clock64() - since > (1ll << 32)) {
-        *fail = 1;
+            for (int e = 0; e < 4; ++e) mma_f8(d, k + 2 * e, q + 2 * e, d_qk, e > 0 ? 1 : c > 0);
+          } else {
+            for (int e = 0; e < left; ++e) mma_f8(d, k + 2 * e, q + 2 * e, d_qk, c > 0 || e > 0);
+          }
+        }
+        if (half.v0 == half.v1) tc_commit(b_empty + 16 * s + 8 * u);
+        if (u == 1 || !a.latent) tc_commit(b_s + 8 * (i & 1));
       }
       __syncwarp();
+    };
+    // ... and of its products with the probabilities.
+    auto values = [&](int i, int u) {
+      const Half half = half_of(a, u);
+      const int steps = (min(a.tile, t1 - t0 - i * a.tile) + 31) >> 5;
+      uint32_t v = smem_desc(base + s * a.stage_bytes) + ((half.is_v ? a.k_chunks : 0) + half.v0) * a.tile * 8;
+      if (elected) {
+        for (int j = half.v0; j < half.v1; ++j, v += a.tile * 8) {
+          const uint32_t d = t_o + j * N;
+          uint32_t p = p_desc, w = v;
+#pragma unroll 2
+          for (int k = 0; k < steps; ++k, p += 256, w += 256)
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t)
+              mma_f8(d, w, p + t * N / 16, t + 1 < kTerms ? d_pv : d_pv5, t > 0 ? 1 : i > 0 || k > 0);
+        }
+        if (half.v0 < half.v1) tc_commit(b_empty + 16 * s + 8 * u);
+        if (u == 1) {
+          tc_commit(b_used + 8 * (i % kTables));
+          tc_commit(b_pv);
+        }
+      }
+      __syncwarp();
+    };
+    // Scores run at most one tile ahead of the softmax (two buffers); each half starts as it
+    // arrives.
+    if (warp == Shape<N>::mma) {
+      bar_wait(b_q, 0, fail);
+      for (int i = 0; i < tiles; ++i) {
+        if (i > 1) bar_wait(b_read + 8 * (i & 1), (i / 2 - 1) & 1, fail);
+#pragma unroll 1
+        for (int u = 0; u < (a.latent ? 2 : 1); ++u) {
+          bar_wait(b_full + 16 * s + 8 * u, turn & 1, fail);
+          fence_async();
+          __syncwarp();
+          tc_after();
+          scores(i, u);
+        }
+        if (++s == a.stages) s = 0, ++turn;
+      }
+    } else {
+      for (int i = 0; i < tiles; ++i) {
+        bar_wait(b_p, i & 1, fail);
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          bar_wait(b_full + 16 * s + 8 * u, turn & 1, fail);
+          fence_async();
+          __syncwarp();
+          tc_after();
+          values(i, u);
+        }
+        if (++s == a.stages) s = 0, ++turn;
+      }
     }
   }
   // ---- join ----------------------------------------------------------------------
@@ -1091,7 +1104,7 @@ constexpr uint32_t kSmemSm = 233472;     // of an SM; a CTA takes its own and 1 
 constexpr uint32_t kSmemCta = 232448;    // at most, static and dynamic
 
 // Tile, stages and offsets for N heads; false where they do not fit in `limit` bytes.
-bool plan_smem(AttendArgs &a, int N, int terms, int tile, uint32_t limit, uint32_t &bytes) {
+bool plan_smem(AttendArgs &a, int N, int terms, int tables, int tile, uint32_t limit, uint32_t &bytes) {
   a.tile = tile;
   a.k_chunks = (a.k_dim + 127) / 128;
   a.v_tiles = (a.v_dim + 127) / 128;
@@ -1103,8 +1116,8 @@ bool plan_smem(AttendArgs &a, int N, int terms, int tile, uint32_t limit, uint32
   // rows beyond a tile that the 128-row products read stay inside: Q and P follow
   const uint32_t over = (128 - tile) * 128;
   const uint32_t rest = q + p + (q + p < over ? over - q - p : 0);
-  // tables: two scales a token, and an address (two with a V part)
-  const uint32_t meta = kTables * tile * (a.latent ? 16 : 24);
+  // tables: two scales a token, and a row or its address (two with a V part)
+  const uint32_t meta = tables * tile * (a.latent ? 16 : 24);
   const uint32_t sums = static_cast<uint32_t>(N) * a.v_dim * 4;
   const uint32_t fixed = rest + meta + 1024;
   if (fixed + 2 * a.stage_bytes > limit) return false;
@@ -1112,7 +1125,7 @@ bool plan_smem(AttendArgs &a, int N, int terms, int tile, uint32_t limit, uint32
   a.off_q = a.stages * a.stage_bytes;
   a.off_p = a.off_q + q;
   a.off_meta = a.off_q + rest;
-  a.off_rows = a.off_meta + kTables * tile * 8;
+  a.off_rows = a.off_meta + tables * tile * 8;
   bytes = std::max(a.off_meta + meta, sums) + 1024;
   return bytes <= limit;
 }
@@ -1180,7 +1193,7 @@ int launch_attend(AttendArgs a, int64_t units, void *stream) {
   const uint32_t least = std::min(whole, kSmemSm / 512 * cols - 1024);
   uint32_t bytes = 0;
   bool ok = false;
-  for (int tile = 128; tile >= 64 && !ok; tile -= 32) ok = plan_smem(a, N, Terms<T>::n, tile, whole, bytes);
+  for (int tile = 128; tile >= 64 && !ok; tile -= 32) ok = plan_smem(a, N, Terms<T>::n, Shape<N>::tables, tile, whole, bytes);
   if (!ok) return HISPARSE_EBOUND;
   bytes = std::max(bytes, least);
   // Split the tokens over a cluster while all clusters still run at once and a CTA keeps 64
@@ -1198,14 +1211,19 @@ int launch_attend(AttendArgs a, int64_t units, void *stream) {
 template <class T>
 int pick_attend(AttendArgs a, int64_t pairs, void *stream) {
   // Heads of a KV head that one CTA takes: enough for the group, at most 64 (32 with
-  // three terms, whose probabilities fill a 128-byte row).
+  // three terms, whose probabilities fill a 128-byte row), and fewer where the widest rows leave no
+  // room for two tiles.
   int n = a.group <= 16 ? 16 : a.group <= 32 || Terms<T>::n == 3 ? 32 : 64;
-  a.hgroups = (a.group + n - 1) / n;
-  const int64_t units = pairs * a.hgroups;
-  if (n == 16) return launch_attend<T, 16>(a, units, stream);
-  if (n == 32) return launch_attend<T, 32>(a, units, stream);
-  if constexpr (Terms<T>::n == 2) return launch_attend<T, 64>(a, units, stream);
-  return HISPARSE_EBOUND;
+  for (;; n /= 2) {
+    a.hgroups = (a.group + n - 1) / n;
+    const int64_t units = pairs * a.hgroups;
+    int rc = HISPARSE_EBOUND;
+    if (n == 16) return launch_attend<T, 16>(a, units, stream);
+    if (n == 32) rc = launch_attend<T, 32>(a, units, stream);
+    if constexpr (Terms<T>::n == 2)
+      if (n == 64) rc = launch_attend<T, 64>(a, units, stream);
+    if (rc != HISPARSE_EBOUND) return rc;
+  }
 }
 
 }  // namespace
@@ -1234,7 +1252,10 @@ int hisparse_attend(const hisparse_attend_args *g, void *stream) {
   if (g->resident && (!aligned16(g->resident) || g->resident_row_stride % 16 ||
                       g->resident_row_stride < row * g->record_tokens))
     return HISPARSE_EINVAL;
-  if (g->record_tokens > 65536 || g->heads > 65535 ||
+  if (g->hot_row_stride > UINT32_MAX || (g->resident && g->resident_row_stride > UINT32_MAX) ||
+      static_cast<int64_t>(g->scale_blocks) * record_columns(r) > INT32_MAX || g->sel_block_tokens > 65535)
+    return HISPARSE_EBOUND;
+  if (g->record_tokens > 65535 || g->heads > 65535 ||
       static_cast<int64_t>(g->num_requests) * g->rows > (1 << 28) ||
       static_cast<int64_t>(g->entries) * g->record_tokens > (1 << 30))
     return HISPARSE_EBOUND;
@@ -1251,13 +1272,13 @@ int hisparse_attend(const hisparse_attend_args *g, void *stream) {
   a.out = g->out; a.out_row = g->out_row_stride; a.out_head = g->out_head_stride;
   a.lse = g->lse; a.sel = g->d_sel; a.slots = g->d_slots;
   a.hot = static_cast<const char *>(g->hot);
-  a.hot_req = g->hot_req_stride; a.hot_row = g->hot_row_stride;
+  a.hot_req = g->hot_req_stride; a.hot_row = static_cast<uint32_t>(g->hot_row_stride);
   a.resident = static_cast<const char *>(g->resident);
-  a.res_rows = g->resident ? g->resident_rows : 0;
-  a.res_row = g->resident_row_stride;
+  a.res_rows = g->resident ? static_cast<uint32_t>(std::min<int64_t>(g->resident_rows, INT32_MAX)) : 0;
+  a.res_row = g->resident ? static_cast<uint32_t>(g->resident_row_stride) : 0;
   a.scales = g->scales; a.scales_req = g->scales_req_stride; a.scale_blocks = g->scale_blocks;
   a.seq_lens = g->d_seq_lens; a.num_reqs = g->d_num_reqs; a.status = g->d_status;
-  a.row_bytes = row;
+  a.row_bytes = static_cast<uint32_t>(row);
   a.quads = FastDiv(r.v_dim / 4);
   const int64_t pairs = static_cast<int64_t>(g->num_requests) * g->rows * r.kv_heads;
   return g->dtype == HISPARSE_BF16 ? pick_attend<__nv_bfloat16>(a, pairs, stream)

@@ -476,6 +476,26 @@ def test_attend_pages_residents_blocks_and_strides(rec, heads):
     assert bool((ow[..., rec.v_dim:] == 0).all())
 
 
+@pytest.mark.parametrize("rec,heads,dtype,tok", [(LATENT, 32, torch.bfloat16, 1), (HEADS, 16, torch.bfloat16, 1),
+                                                 (HEADS, 8, torch.float16, 4)])
+def test_attend_residents_mixed_every_way(rec, heads, dtype, tok):
+    """Rows of both stores side by side: runs of one, alternating ones, masked ones between."""
+    g = _gen(31)
+    c = _attend_case(rec, heads, dtype, 3, 1, 320, tok=tok, pad=0.15)
+    B = c["hot"].shape[1] - 1
+    res = (_randn(g, 77, tok * rec.row_bytes) * 60).clamp(-448, 448).to(E4M3).view(torch.uint8)
+    pick = torch.randint(0, 77, (3, 320), device="cuda", generator=g).int() + B + 1
+    far = torch.zeros(3, 320, dtype=torch.bool, device="cuda")
+    far[:, 64:128] = True
+    far[:, 128:200:2] = True
+    far[:, 200:260] = torch.rand(3, 60, device="cuda", generator=g) < 0.5
+    c["slots"] = torch.where(far & (c["slots"] >= 0), pick, c["slots"]).contiguous()
+    assert _attend(c, record_tokens=tok, resident=res) == 0
+    want = _attend64(rec, c["q"], c["sel"], c["slots"], c["hot"], c["scales"], rec.k_dim ** -0.5, tok=tok,
+                     resident=res)
+    _attend_close(c["out"], c["lse"], want, dtype)
+
+
 def test_attend_reports_what_is_out_of_range():
     c = _attend_case(HEADS, 8, torch.bfloat16, 2, 1, 50, pad=0.0)
     B = c["hot"].shape[1] - 1
