@@ -93,7 +93,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {  // sus
 __device__ __noinline__ void bar_wait_long(uint32_t bar, uint32_t parity, volatile int *fail) {
   const long long start = clock64();
   while (!bar_try(bar, parity) && !*fail) {
-    if (clock64() - start > (1ll << 32)) *fail = 1;
+    if (clock64() - start > (1ll << 30)) *fail = 1;
   }
 }
 __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile int *fail) {
@@ -226,11 +226,6 @@ __device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float ld_peer(uint32_t addr) {
-  float r;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(addr) : "memory");
-  return r;
-}
 __device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
   float4 r;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -356,17 +351,28 @@ __device__ __forceinline__ void gather_columns(uint32_t table, uint32_t off, uin
   const int tl = lane >> kLw;
   const int sub = kAtOnce > 1 ? tl >> 3 : 0;      // the group of a turn that the lane is in
   const int row = kAtOnce > 1 ? tl & 7 : tl;
+  constexpr int kBatch = kTurns >= 4 ? 2 : 3;  // turns of groups whose addresses are read together
 #pragma unroll 1
-  for (int g = warp; g < groups; g += kWarps * kAtOnce) {
-    const int mine = g + sub * kWarps;
-    if (kAtOnce > 1 && mine >= groups) continue;
-    const uint32_t src = table + (mine * 8 + row) * 8;
-    const uint32_t to = (dst ^ ((row & 7) << 4)) + (mine * 8 + row) * 128;
-    uint64_t p[kTurns];
+  for (int g = warp; g < groups; g += kBatch * kWarps * kAtOnce) {
+    uint64_t p[kBatch][kTurns];
 #pragma unroll
-    for (int u = 0; u < kTurns; ++u) asm volatile("ld.shared.b64 %0, [%1];" : "=l"(p[u]) : "r"(src + u * kDt * 8));
+    for (int b = 0; b < kBatch; ++b) {
+      const int mine = g + (b * kAtOnce + sub) * kWarps;
+      if (mine < groups) {
 #pragma unroll
-    for (int u = 0; u < kTurns; ++u) cp_async16((to ^ (u * kDt << 4)) + u * kDt * 128, p[u] + off);
+        for (int u = 0; u < kTurns; ++u)
+          asm volatile("ld.shared.b64 %0, [%1];" : "=l"(p[b][u]) : "r"(table + (mine * 8 + row + u * kDt) * 8));
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int mine = g + (b * kAtOnce + sub) * kWarps;
+      const uint32_t to = (dst ^ ((row & 7) << 4)) + (mine * 8 + row) * 128;
+      if (mine < groups) {
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) cp_async16((to ^ (u * kDt << 4)) + u * kDt * 128, p[b][u] + off);
+      }
+    }
   }
 }
 
@@ -457,8 +463,9 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
   __shared__ uint64_t s_bars[4 * kMaxStages + 3 * kTables + 7];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
-  __shared__ float s_l[N], s_f[N], s_d[N], s_wmax[4][N], s_w[kMaxCluster * N];
-  __shared__ __align__(16) float s_qf[N], s_m[N];
+  __shared__ float s_l[N], s_d[N], s_wmax[4][N], s_w[N];
+  __shared__ float2 s_pair[N];
+  __shared__ __align__(16) float s_qf[N], s_m[N], s_f[N];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = smem_u32(s_bars);
   const uint32_t b_full = bars, b_empty = bars + 16 * kMaxStages;  // [stage][half]
@@ -481,7 +488,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     bar_init(b_read + 8, 32 * kSoft);
     bar_init(b_p, 32 * kSoft);
     bar_init(b_pv, 1);
-    bar_init(b_q, 32 * (kSoft + kGather));
+    bar_init(b_q, 32 * (kSoft + 2));
     for (int t = 0; t < kTables; ++t) {
       bar_init(b_tab + 8 * t, 32 * Shape<N>::looks);
       bar_init(b_meta + 8 * t, 32 * Shape<N>::looks);
@@ -490,7 +497,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     s_fail = 0;
   }
   for (int i = tid; i < 2 * a.stages; i += kThreads) {
-    bar_init(b_full + 8 * i, 32 * kGather);
+    bar_init(b_full + 8 * i, 32 * kGather / 2);
     bar_init(b_empty + 8 * i, 1);
   }
   for (int c = tid; c < N; c += kThreads) s_m[c] = 0.f;
@@ -510,6 +517,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   pdl_wait();
   if (a.num_reqs && req >= *a.num_reqs) return;  // the whole cluster
+  if (a.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if (warp == Shape<N>::mma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
                  "r"(a.tmem_cols)
@@ -529,12 +537,12 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
   const int64_t entry0 = qrow * a.entries;
   volatile int *fail = &s_fail;
 
-  // Query heads of this group into e4m3 terms, by the softmax and gather warps while the
-  // first rows are looked up.
+  // Query heads of this group into e4m3 terms, by the softmax and product warps while the first
+  // rows come.
   auto make_q = [&](int w) {
     const int vecs = a.k_dim >> 3;
     const T *q0 = static_cast<const T *>(a.q) + qrow * a.q_row;
-    constexpr int kWarps = kSoft + kGather, kBatch = (N + kWarps - 1) / kWarps;
+    constexpr int kWarps = kSoft + 2, kBatch = (N + kWarps - 1) / kWarps;
     {
       const int n0 = w;
       uint4 v[kBatch][3];  // all of a warp's heads in flight together
@@ -576,7 +584,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     bar_arrive(b_q);
   };
 
-  if (warp < Shape<N>::mma) make_q(warp);
+  if (warp < kSoft || (warp >= Shape<N>::mma && warp < Shape<N>::look)) make_q(warp < kSoft ? warp : warp - kGather);
 
   if (warp < kSoft) {
     // ---- softmax ---------------------------------------------------------------
@@ -744,42 +752,42 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     __syncwarp();
   } else if (warp < Shape<N>::mma) {
     // ---- gather ------------------------------------------------------------------
-    // A tile comes in halves, each as soon as its place is free and with its own arrival.
-    const int gw = warp - kSoft;
+    // A tile comes in halves, each as soon as its place is free and with its own arrival and its own
+    // half of the warps, as a half is mostly latency; a warp takes every kShare-th group of 8 rows.
+    constexpr int kShare = kGather / 2;
+    const int u = (warp - kSoft) & 1, gw = (warp - kSoft) >> 1;
+    const Half half = half_of(a, u);
+    const int cols = min(8 * half.c1, (half.is_v ? a.v_dim : a.k_dim) >> 4);
+    const uint32_t table = base + a.off_rows + (half.is_v ? kTables * a.tile * 8 : 0);
+    uint32_t st = base + (half.is_v ? a.k_chunks * a.tile * 128 : 0);
     int s = 0, turn = 0;  // the tile's stage, and how often the stages went round
     for (int i = 0; i < tiles; ++i) {
-      const int groups = (min(a.tile, t1 - t0 - i * a.tile) + 31) >> 5 << 2;  // of 8 rows
-      const uint32_t st = base + s * a.stage_bytes;
-      const uint32_t table = base + a.off_rows + i % kTables * a.tile * 8;
+      const int groups = (min(a.tile, t1 - t0 - i * a.tile) + 31) >> 5 << 2;
+      const uint32_t rows = table + i % kTables * a.tile * 8;
       bar_wait(b_tab + 8 * (i % kTables), (i / kTables) & 1, fail);
-#pragma unroll 1
-      for (int u = 0; u < 2; ++u) {
-        const Half half = half_of(a, u);
-        const uint32_t full = b_full + 16 * s + 8 * u;
-        const uint32_t to = st + (half.is_v ? a.k_chunks * a.tile * 128 : 0);
-        if (turn > 0) bar_wait(b_empty + 16 * s + 8 * u, (turn - 1) & 1, fail);
-        __syncwarp();
-        // 16-byte copies; of the groups of 8 rows a warp takes every kGather-th.
-        const int cols = min(8 * half.c1, (half.is_v ? a.v_dim : a.k_dim) >> 4);
-        const uint32_t rows = table + (half.is_v ? kTables * a.tile * 8 : 0);
-        for (int col0 = 8 * half.c0; col0 < cols;) {
-          const int left = cols - col0, lw = left >= 32 ? 5 : 31 - __clz(left);
-          const int j = col0 + (lane & ((1 << lw) - 1));
-          const uint32_t dst = to + (j >> 3) * a.tile * 128 + ((j & 7) << 4);
-          switch (lw) {
-            case 5: gather_columns<5, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
-            case 4: gather_columns<4, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
-            case 3: gather_columns<3, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
-            case 2: gather_columns<2, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
-            case 1: gather_columns<1, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
-            default: gather_columns<0, kGather>(rows, 16 * j, dst, groups, gw, lane); break;
-          }
-          col0 += 1 << lw;
+      if (turn > 0) bar_wait(b_empty + 16 * s + 8 * u, (turn - 1) & 1, fail);
+      for (int col0 = 8 * half.c0; col0 < cols;) {
+        const int left = cols - col0, lw = left >= 32 ? 5 : 31 - __clz(left);
+        const int j = col0 + (lane & ((1 << lw) - 1));
+        const uint32_t dst = st + (j >> 3) * a.tile * 128 + ((j & 7) << 4);
+        switch (lw) {
+          case 5: gather_columns<5, kShare>(rows, 16 * j, dst, groups, gw, lane); break;
+          case 4: gather_columns<4, kShare>(rows, 16 * j, dst, groups, gw, lane); break;
+          case 3: gather_columns<3, kShare>(rows, 16 * j, dst, groups, gw, lane); break;
+          case 2: gather_columns<2, kShare>(rows, 16 * j, dst, groups, gw, lane); break;
+          case 1: gather_columns<1, kShare>(rows, 16 * j, dst, groups, gw, lane); break;
+          default: gather_columns<0, kShare>(rows, 16 * j, dst, groups, gw, lane); break;
         }
-        cp_arrive(full);
+        col0 += 1 << lw;
       }
-      if (++s == a.stages) s = 0, ++turn;
+      cp_arrive(b_full + 16 * s + 8 * u);
+      st += a.stage_bytes;
+      if (++s == a.stages) {
+        s = 0, ++turn;
+        st -= a.stages * a.stage_bytes;
+      }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= Shape<N>::look) {
     // ---- rows: slot -> address, position -> scales, tiles ahead of their copies --------
     const uint32_t k_at = kvh * a.k_dim, v_at = a.kv_heads * a.k_dim + kvh * a.v_dim;
@@ -825,7 +833,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     // In steps of a token a lane, `per` of them a tile.  Loads are kAhead steps ahead of their
     // use: of slots and positions, and of the scales after the addresses are out; each of kAhead
     // steps in turn has its own registers, so that none waits for another's load.
-    constexpr int kLooks = Shape<N>::looks, kAhead = 4;
+    constexpr int kLooks = Shape<N>::looks, kAhead = 2;
     const int per = (a.tile + 32 * kLooks - 1) / (32 * kLooks), steps = tiles * per;
     const int mine = (warp - Shape<N>::look) * 32 + lane;
     struct Step {
@@ -876,26 +884,20 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       x.k = ld_if(sc, now.row != 0, 0x7fffffff);
       x.v = ld_if(sc + v_col, now.row != 0, 0);
     };
-    Step x0, x1, x2, x3;
+    Step x0, x1;
     fetch(x0, at, as), advance(at, as);
     fetch(x1, at, as), advance(at, as);
-    fetch(x2, at, as), advance(at, as);
-    fetch(x3, at, as), advance(at, as);
 #pragma unroll 1
     for (int n = 0; n < steps; n += kAhead) {
       step(x0, n);
       step(x1, n + 1);
-      step(x2, n + 2);
-      step(x3, n + 3);
     }
-    // the last kAhead steps' scales, in order
-#pragma unroll 1
-    for (int n = max(0, steps - kAhead); n < steps; ++n) {
-      const int w = n & 3;
-      const Step x = w == 0 ? x0 : w == 1 ? x1 : w == 2 ? x2 : x3;
-      put_scales(x, bt, bs);
+    // the last two steps' scales, in order
+    if (steps > 1) {
+      put_scales(steps & 1 ? x1 : x0, bt, bs);
       advance(bt, bs);
     }
+    if (steps > 0) put_scales(steps & 1 ? x0 : x1, bt, bs);
   } else {
     // ---- products: a warp for the scores and one for the values; one lane issues -----------
     const uint32_t d_qk = mma_desc(kQ, false, false);
@@ -968,7 +970,8 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
         bar_wait(b_p, i & 1, fail);
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
-          bar_wait(b_full + 16 * s + 8 * u, turn & 1, fail);
+          // (a half without values may be gone and filled again by now: it is not waited for)
+          if (half_of(a, u).v0 < half_of(a, u).v1) bar_wait(b_full + 16 * s + 8 * u, turn & 1, fail);
           fence_async();
           __syncwarp();
           tc_after();
@@ -980,65 +983,70 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
   }
   // ---- join ----------------------------------------------------------------------
   // Every product is done (the softmax warps' last wait), so the stages and Q hold
-  // nothing any more.  A lone CTA writes its results from TMEM; in a cluster they take the
-  // CTA's sums [N][v_dim] for the others to read.
+  // nothing any more.  A lone CTA's results pass through them in their type; in a cluster they
+  // take the CTA's sums [N][v_dim] for the others to read, and each CTA joins a share of the heads.
+  // (Loops rather than unrolled runs: this is executed once, at the instruction cache's pace.)
   __syncwarp();
+  const bool lone = a.cluster == 1;
+  const int share = N / a.cluster, n0 = static_cast<int>(rank) * share;
+  if (!lone) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all CTAs run
   __syncthreads();
   T *out = static_cast<T *>(a.out) + qrow * a.out_row;
   const int h0 = kvh * a.group + hg * N, heads = min(N, a.group - static_cast<int>(hg) * N);
+  if (!lone && tid < N) {  // a column's offset and sum to the CTA that joins it
+    const uint32_t to = peer(smem_u32(&s_pair[rank * share + tid % share]), tid / share);
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(s_m[tid]), "f"(s_l[tid]) : "memory");
+  }
   if (warp < kSoft) {
     tc_after();
-    const int grp = warp >> 2, wl = warp & 3, c0 = grp * NC;
+    const int wl = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
-    for (int j = 0; j < a.v_tiles; ++j) {
-      const int d = j * 128 + wl * 32 + lane;
-      float o[NC];
-      if (tiles > 0) {
+#pragma unroll 1
+    for (int c = (warp >> 2) * NC; c < ((warp >> 2) + 1) * NC; c += 16) {
+      float f[16];
 #pragma unroll
-        for (int c = 0; c < NC; c += 16)
-          tc_ld16(t_o + lanes + j * N + c0 + c, reinterpret_cast<uint32_t *>(o + c));
-#pragma unroll
-        for (int c = 0; c < NC; c += 16) tc_wait_ld16(reinterpret_cast<uint32_t *>(o + c));
-      } else {
-#pragma unroll
-        for (int c = 0; c < NC; ++c) o[c] = 0.f;
+      for (int e = 0; e < 16; e += 4) {
+        const float4 x = ld_shared4(smem_u32(s_f + c + e));
+        f[e] = x.x, f[e + 1] = x.y, f[e + 2] = x.z, f[e + 3] = x.w;
       }
-      if (d >= a.v_dim) continue;
-      if (a.cluster == 1) {
+#pragma unroll 1
+      for (int j = 0; j < a.v_tiles; ++j) {
+        const int d = j * 128 + wl * 32 + lane;
+        uint32_t o[16];
+        if (tiles > 0) {
+          tc_ld16(t_o + lanes + j * N + c, o);
+          tc_wait_ld16(o);
+        } else {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const float f = s_f[c0 + c];
-          o[c] = f != 0.f ? o[c] * f : 0.f;
+          for (int e = 0; e < 16; ++e) o[e] = 0;
         }
-        T *p = reinterpret_cast<T *>(smem_raw + (base - smem_u32(smem_raw))) + c0 * a.v_dim + d;
+        if (d >= a.v_dim) continue;
+        if (lone) {
+          const uint32_t to = base + (c * a.v_dim + d) * static_cast<uint32_t>(sizeof(T));
+          uint16_t h[16];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) p[c * a.v_dim] = from_f32<T>(o[c]);
-      } else {
+          for (int e = 0; e < 16; ++e) {
+            const T x = from_f32<T>(f[e] != 0.f ? __uint_as_float(o[e]) * f[e] : 0.f);
+            h[e] = *reinterpret_cast<const uint16_t *>(&x);
+          }
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((c0 + c) * a.v_dim + d) * 4), "f"(o[c]) : "memory");
+          for (int e = 0; e < 16; ++e)
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + e * a.v_dim * static_cast<uint32_t>(sizeof(T))), "h"(h[e]) : "memory");
+        } else {
+          const uint32_t to = base + (c * a.v_dim + d) * 4;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + e * a.v_dim * 4), "r"(o[e]) : "memory");
+        }
       }
     }
     __syncwarp();
     tc_before();
   }
-  if (a.cluster == 1) {
-    if (a.lse && tid < heads) {
-      const float z = s_l[tid];
-      a.lse[qrow * a.heads + h0 + tid] =
-          z > 0.f || z != z ? (s_m[tid] + log2f(z)) * 0.6931471805599453f : -INFINITY;
-    }
+  __syncwarp();
+  if (lone) {
     __syncthreads();
-    const T *p = reinterpret_cast<const T *>(smem_raw + (base - smem_u32(smem_raw)));
-    const uint32_t total = heads * (a.quads.d >> 1);
-    for (uint32_t i = tid; i < total; i += kThreads) {
-      uint32_t n, d;
-      a.quads.divmod(2 * i, n, d);
-      *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(h0 + n) * a.out_head + 4 * d) =
-          *reinterpret_cast<const uint4 *>(p + n * a.v_dim + 4 * d);
-    }
   } else {
-    __syncwarp();
     cluster_sync();
   }
   if (warp == Shape<N>::mma) {
@@ -1046,57 +1054,67 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(a.tmem_cols));
   }
   if (tid == 0 && s_fail && a.status) atomicOr(a.status, HISPARSE_ERR_WAIT);
-  if (a.cluster == 1) return;
-  // Each CTA joins a share of the heads: weights 2^(m_r - max m) of the CTAs' sums.
-  const int share = N / a.cluster, n0 = static_cast<int>(rank) * share;
-  if (tid < share) {
-    const int n = n0 + tid;
-    float m = -INFINITY, z = 0.f;
-#pragma unroll 4
-    for (int r = 0; r < a.cluster; ++r) {
-      const float x = ld_peer(peer(smem_u32(&s_m[n]), r));
-      s_w[r * N + tid] = x;
-      m = fmaxf(m, x);
+  if (!lone) {
+    // weights 2^(m_r - max m) of the CTAs' sums
+    if (tid < share) {
+      float m = kNone, z = 0.f;
+#pragma unroll 1
+      for (int r = 0; r < a.cluster; ++r) m = fmaxf(m, s_pair[r * share + tid].x);
+#pragma unroll 1
+      for (int r = 0; r < a.cluster; ++r) {
+        const float2 x = s_pair[r * share + tid];
+        const float w = ex2(x.x - m);
+        s_w[r * share + tid] = w;
+        z = fmaf(w, x.y, z);
+      }
+      s_m[tid] = m;
+      s_l[tid] = z;
+      s_f[tid] = z > 0.f || z != z ? 1.f / z : 0.f;
     }
-#pragma unroll 4
-    for (int r = 0; r < a.cluster; ++r) {
-      const float x = s_w[r * N + tid], y = ld_peer(peer(smem_u32(&s_l[n]), r));
-      const float w = ex2(x - m);
-      s_w[r * N + tid] = w;
-      z = fmaf(w, y, z);
-    }
-    s_qf[tid] = z > 0.f || z != z ? 1.f / z : 0.f;
-    if (a.lse && n < heads)
-      a.lse[qrow * a.heads + h0 + n] = z > 0.f || z != z ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
+    __syncthreads();
   }
-  __syncthreads();
-  for (uint32_t i = tid; i < share * a.quads.d; i += kThreads) {
+  const int mine = lone ? heads : min(share, heads - n0), first = lone ? 0 : n0;
+  if (a.lse && tid < mine) {
+    const float z = s_l[tid];
+    a.lse[qrow * a.heads + h0 + first + tid] =
+        z > 0.f || z != z ? (s_m[tid] + log2f(z)) * 0.6931471805599453f : -INFINITY;
+  }
+  if (lone) {
+    const uint32_t total = heads * (a.quads.d >> 1);
+    for (uint32_t i = tid; i < total; i += kThreads) {
+      uint32_t n, d;
+      a.quads.divmod(2 * i, n, d);
+      const float4 v = ld_shared4(base + (n * a.v_dim + 4 * d) * sizeof(T));
+      *reinterpret_cast<float4 *>(out + static_cast<int64_t>(h0 + n) * a.out_head + 4 * d) = v;
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int i = tid; i < mine * static_cast<int>(a.quads.d); i += kThreads) {
     uint32_t nn, d;
     a.quads.divmod(i, nn, d);
-    if (n0 + static_cast<int>(nn) >= heads) continue;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     const uint32_t at = base + ((n0 + nn) * a.v_dim + 4 * d) * 4;
 #pragma unroll 1
     for (int r0 = 0; r0 < a.cluster; r0 += 4) {
       float4 v[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (r0 + r < a.cluster) v[r] = ld_peer4(peer(at, r0 + r));
+      for (int r = 0; r < 4; ++r) v[r] = ld_peer4(peer(at, min(r0 + r, a.cluster - 1)));
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        if (r0 + r >= a.cluster) break;
-        const float w = s_w[(r0 + r) * N + nn];
+        const float w = r0 + r < a.cluster ? s_w[(r0 + r) * share + nn] : 0.f;
         acc[0] = fmaf(w, v[r].x, acc[0]);
         acc[1] = fmaf(w, v[r].y, acc[1]);
         acc[2] = fmaf(w, v[r].z, acc[2]);
         acc[3] = fmaf(w, v[r].w, acc[3]);
       }
     }
-    const float inv = s_qf[nn];
+    const float inv = s_f[nn];
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = inv != 0.f ? acc[e] * inv : 0.f;
     store_vec<T, 4>(out + static_cast<int64_t>(h0 + n0 + nn) * a.out_head + 4 * d, acc);
   }
+  __syncwarp();
   cluster_sync();  // peers have read this CTA's shared memory
 }
 
@@ -1162,12 +1180,34 @@ int active_clusters(const void *fn, int threads, uint32_t bytes, int c, int dev)
   return n;
 }
 
+struct Plan {
+  AttendArgs a;
+  int64_t units;
+  double cycles;
+  uint32_t bytes;
+};
+
+// How N heads a CTA and a cluster of how many CTAs would do, in estimated cycles.
+//
+// A wave of CTAs costs its start (11,000 cycles to the first scores, 90 for each head's q),
+// a turn for every tile, and the join of a cluster (N * v_dim sums a CTA at the 14 B/cycle of
+// distributed shared memory).  A tile's turn is the largest of: its copies, at 27 B/cycle; its
+// products, 32 cycles for the rows and a quarter for each column, 40 at least; the softmax;
+// and the 7,400 cycles from a free stage to the next over the number of stages.  Wider groups read a row
+// fewer times, narrower ones make more CTAs.  For 8 requests of 2048 tokens and 64 heads that
+// reads, against what was measured (us): 16 heads by 4 CTAs 15 (16), 32 by 4 22 (22), 64 by 8
+// 20 (22), 16 by 1 32 (36); for 64 requests of 128 heads: 64 heads by 1 51 (69), 32 by 1 99 (108),
+// 16 by 1 129 (152).
 template <class T, int N>
-int launch_attend(AttendArgs a, int64_t units, void *stream) {
+int plan_attend(const AttendArgs &args, int64_t pairs, Plan &best) {
+  AttendArgs a = args;
+  a.hgroups = (a.group + N - 1) / N;
+  const int64_t units = pairs * a.hgroups;
+  constexpr int kTerms = Terms<T>::n;
   // TMEM: two score buffers and the sums, a power of two of columns.
   int cols = 32;
   a.v_tiles = (a.v_dim + 127) / 128;
-  while (cols < 2 * Terms<T>::n * N + a.v_tiles * N) cols *= 2;
+  while (cols < 2 * kTerms * N + a.v_tiles * N) cols *= 2;
   a.tmem_cols = cols;
   const int64_t tokens = static_cast<int64_t>(a.entries) * a.rec_tokens.d;
   auto fn = attend_kernel<T, N>;
@@ -1181,49 +1221,75 @@ int launch_attend(AttendArgs a, int64_t units, void *stream) {
     fixed.store(static_cast<uint32_t>(fa.sharedSizeBytes));
     HS_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kSmemCta - static_cast<uint32_t>(fa.sharedSizeBytes)));
-    HS_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 cudaSharedmemCarveoutMaxShared));
     HS_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     ready.fetch_or(1ull << (dev & 63));
   }
-  // CTAs that share an SM share its TMEM: each takes at least as large a part of
+  // CTAs that share an SM would share its TMEM: each takes at least as large a part of
   // the SM's shared memory as of its TMEM, so that no CTA of a cluster waits for columns that
   // a CTA of another cluster holds.
   const uint32_t whole = kSmemCta - fixed.load();
   const uint32_t least = std::min(whole, kSmemSm / 512 * cols - 1024);
   uint32_t bytes = 0;
   bool ok = false;
-  for (int tile = 128; tile >= 64 && !ok; tile -= 32) ok = plan_smem(a, N, Terms<T>::n, Shape<N>::tables, tile, whole, bytes);
-  if (!ok) return HISPARSE_EBOUND;
+  for (int tile = 128; tile >= 64 && !ok; tile -= 32) ok = plan_smem(a, N, kTerms, Shape<N>::tables, tile, whole, bytes);
+  if (!ok) return HISPARSE_OK;  // the widest rows leave no room for two tiles of so many heads
   bytes = std::max(bytes, least);
-  // Split the tokens over a cluster while all clusters still run at once and a CTA keeps 64
-  // tokens or more.
-  int c = 1;
-  while (c < kMaxCluster && tokens >= static_cast<int64_t>(c) * 2 * 64 &&
-         units <= active_clusters(reinterpret_cast<const void *>(fn), Shape<N>::threads, bytes, 2 * c, dev))
-    c *= 2;
-  a.cluster = c;
-  a.per_cta = static_cast<int>(((tokens + c - 1) / c + 31) / 32 * 32);
-  if (units * c > 0x7fffffff) return HISPARSE_EBOUND;
-  return launch_pdl(fn, dim3(static_cast<unsigned>(units * c)), dim3(Shape<N>::threads), bytes, stream, c, a);
+  const double copy = 400 + a.tile * (a.k_dim + (a.latent ? 0 : a.v_dim)) / 27.0;
+  const double products = (a.k_dim + 31) / 32 * std::max(40.0, 32 + kTerms * N / 4.0) +
+                          a.v_tiles * (a.tile / 32) * kTerms * std::max(40.0, 32 + N / 4.0);
+  const double turn = std::max({copy, products, N > 32 ? 2000.0 : 1200.0, 7400.0 / a.stages});
+  for (int c = 1; c <= kMaxCluster; c *= 2) {
+    if (c > 1 && tokens < 64 * c) break;
+    const int at_once = active_clusters(reinterpret_cast<const void *>(fn), Shape<N>::threads, bytes, c, dev);
+    if (at_once < 1) continue;
+    const int64_t waves = (units + at_once - 1) / at_once;
+    const int64_t per = ((tokens + c - 1) / c + 31) / 32 * 32;
+    const double join = c > 1 ? 2500 + N * a.v_dim * 4.0 * (c - 1) / c / 14 : 0;
+    const double cycles = waves * (11000 + 90.0 * N + turn * ((per + a.tile - 1) / a.tile) + join);
+    if (cycles < best.cycles) {
+      a.cluster = c;
+      a.per_cta = static_cast<int>(per);
+      best = {a, units, cycles, bytes};
+    }
+  }
+  return HISPARSE_OK;
+}
+
+template <class T, int N>
+int launch_attend(const Plan &p, void *stream) {
+  const int64_t ctas = p.units * p.a.cluster;
+  if (ctas > 0x7fffffff) return HISPARSE_EBOUND;
+  return launch_pdl(attend_kernel<T, N>, dim3(static_cast<unsigned>(ctas)), dim3(Shape<N>::threads), p.bytes, stream,
+                    p.a.cluster, p.a);
 }
 
 template <class T>
-int pick_attend(AttendArgs a, int64_t pairs, void *stream) {
-  // Heads of a KV head that one CTA takes: enough for the group, at most 64 (32 with
-  // three terms, whose probabilities fill a 128-byte row), and fewer where the widest rows leave no
-  // room for two tiles.
-  int n = a.group <= 16 ? 16 : a.group <= 32 || Terms<T>::n == 3 ? 32 : 64;
-  for (;; n /= 2) {
-    a.hgroups = (a.group + n - 1) / n;
-    const int64_t units = pairs * a.hgroups;
-    int rc = HISPARSE_EBOUND;
-    if (n == 16) return launch_attend<T, 16>(a, units, stream);
-    if (n == 32) rc = launch_attend<T, 32>(a, units, stream);
-    if constexpr (Terms<T>::n == 2)
-      if (n == 64) rc = launch_attend<T, 64>(a, units, stream);
-    if (rc != HISPARSE_EBOUND) return rc;
+int pick_attend(const AttendArgs &a, int64_t pairs, void *stream) {
+  Plan best = {};
+  best.cycles = 1e300;
+  int n = 0;
+  // 64 heads with two terms at most: three of 64 do not fit a 128-byte row of probabilities.
+  double before = best.cycles;
+  auto took = [&](int heads) {
+    if (best.cycles < before) n = heads;
+    before = best.cycles;
+  };
+  if (const int rc = plan_attend<T, 16>(a, pairs, best)) return rc;
+  took(16);
+  if (a.group > 16) {
+    if (const int rc = plan_attend<T, 32>(a, pairs, best)) return rc;
+    took(32);
   }
+  if constexpr (Terms<T>::n == 2) {
+    if (a.group > 32) {
+      if (const int rc = plan_attend<T, 64>(a, pairs, best)) return rc;
+      took(64);
+    }
+    if (n == 64) return launch_attend<T, 64>(best, stream);
+  }
+  if (n == 32) return launch_attend<T, 32>(best, stream);
+  if (n == 16) return launch_attend<T, 16>(best, stream);
+  return HISPARSE_EBOUND;
 }
 
 }  // namespace

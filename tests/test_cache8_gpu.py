@@ -401,6 +401,20 @@ def test_attend(rec, heads, R, V, n, dtype):
     assert torch.equal(first, c["out"]) and torch.equal(lse, c["lse"])
 
 
+@pytest.mark.parametrize("rec,heads", [(HEADS, 16), (cache8.Records(2, 192, 128, 16), 8), (LATENT, 16)])
+def test_attend_many_tiles_of_many_rows(rec, heads):
+    """So many rows that none is split, each long enough to go round every stage and table of a
+    CTA several times."""
+    c = _attend_case(rec, heads, torch.bfloat16, 64, 1, 3001)
+    assert _attend(c) == 0
+    first = c["out"].clone()
+    assert _attend(c) == 0 and torch.equal(first, c["out"])
+    some = [0, 37, 63]
+    want = _attend64(rec, c["q"][some], c["sel"][some], c["slots"][some], c["hot"][some], c["scales"][some],
+                     rec.k_dim ** -0.5)
+    _attend_close(c["out"][some], c["lse"][some], want, torch.bfloat16)
+
+
 @pytest.mark.parametrize("rec,heads", [(LATENT, 64), (HEADS, 16)])
 def test_attend_long(rec, heads):
     """One request whose whole long selection is attended, and the same with a peaked
