@@ -1112,7 +1112,10 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     const float inv = s_f[nn];
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = inv != 0.f ? acc[e] * inv : 0.f;
-    store_vec<T, 4>(out + static_cast<int64_t>(h0 + n0 + nn) * a.out_head + 4 * d, acc);
+    Vec<T, 4> o;
+    o.set_pair(0, acc[0], acc[1]);
+    o.set_pair(1, acc[2], acc[3]);
+    *reinterpret_cast<Vec<T, 4> *>(out + static_cast<int64_t>(h0 + n0 + nn) * a.out_head + 4 * d) = o;
   }
   __syncwarp();
   cluster_sync();  // peers have read this CTA's shared memory

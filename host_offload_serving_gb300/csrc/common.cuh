@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "hisparse.h"
 
@@ -105,23 +106,41 @@ __device__ __forceinline__ __nv_bfloat16 from_f32(float x) { return __float2bflo
 template <>
 __device__ __forceinline__ __half from_f32(float x) { return __float2half_rn(x); }
 
-// N contiguous elements (N * sizeof(T) bytes, naturally aligned) to and from 32 bits.
+// N contiguous elements, kept in the words they are loaded as (N * sizeof(T) bytes, naturally
+// aligned up to 16), so that they cost no more registers than that until they are used.
 template <class T, int N>
 struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Vec {
-  T e[N];
+  static constexpr int words = sizeof(T) * N / 4;
+  uint32_t w[words];
+  __device__ __forceinline__ float2 pair(int i) const;          // elements 2i, 2i + 1 in 32 bits
+  __device__ __forceinline__ void set_pair(int i, float x, float y);  // rounded to T
+};
+template <class T>
+struct alignas(sizeof(T)) Vec<T, 1> {
+  T e;
 };
 template <class T, int N>
-__device__ __forceinline__ void load_vec(const T *p, float (&v)[N]) {
-  const Vec<T, N> x = *reinterpret_cast<const Vec<T, N> *>(p);
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = to_f32<T>(x.e[i]);
+__device__ __forceinline__ float2 Vec<T, N>::pair(int i) const {
+  if constexpr (sizeof(T) == 4) {
+    return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  } else if constexpr (std::is_same_v<T, __half>) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+  } else {  // the upper 16 bits of a float
+    return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
 }
 template <class T, int N>
-__device__ __forceinline__ void store_vec(T *p, const float (&v)[N]) {
-  Vec<T, N> x;
-#pragma unroll
-  for (int i = 0; i < N; ++i) x.e[i] = from_f32<T>(v[i]);
-  *reinterpret_cast<Vec<T, N> *>(p) = x;
+__device__ __forceinline__ void Vec<T, N>::set_pair(int i, float x, float y) {
+  if constexpr (sizeof(T) == 4) {
+    w[2 * i] = __float_as_uint(x);
+    w[2 * i + 1] = __float_as_uint(y);
+  } else if constexpr (std::is_same_v<T, __half>) {
+    const __half2 h = __floats2half2_rn(x, y);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
 }
 
 // cos and sin of the phase position * turns, a 64-bit fraction of a turn that

@@ -6,14 +6,38 @@
 
 namespace {
 
-constexpr int kRotThreads = 256;
-constexpr int kRotBatch = 2;  // units a thread reads before it writes the first
+// Cosines and sines of `tokens` tokens in shared memory, P pairs to a unit: laid out so that lanes
+// whose units, then tokens, follow one another read 16 bytes each side by side.  (Pairs in their
+// own order cost four times the reads.)
+template <int P>
+__device__ __forceinline__ int table_at(int pair, int token, int tokens, int units) {
+  if (P == 1) return token * units + pair;
+  const int u = pair / P, e = pair % P;
+  return ((e >> 1) * tokens + token) * 2 * units + 2 * u + (e & 1);
+}
+template <int P>
+__device__ __forceinline__ void table_read(const float2 *cs, int unit, int token, int tokens, int units,
+                                           float2 (&w)[P]) {
+  if constexpr (P == 1) {
+    w[0] = cs[token * units + unit];
+  } else {
+#pragma unroll
+    for (int e = 0; e < P; e += 2) {
+      const float4 x = *reinterpret_cast<const float4 *>(cs + ((e >> 1) * tokens + token) * 2 * units + 2 * unit);
+      w[e] = make_float2(x.x, x.y);
+      w[e + 1] = make_float2(x.z, x.w);
+    }
+  }
+}
+
+constexpr int kRotThreads = 384;  // two CTAs of 80 registers a thread to an SM
+constexpr int kRotTable = 48 * 1024;  // bytes of cosines and sines a CTA may hold
 
 struct RotTensor {
   const void *x;
   void *y;
   int64_t xt, xh, yt, yh;
-  FastDiv units;      // per head: half / V rotating ones, then those only copied
+  FastDiv units;      // per head: the rotating ones, then those only copied
   uint32_t per_token; // units of a token: heads * units per head
 };
 struct RotArgs {
@@ -21,120 +45,125 @@ struct RotArgs {
   const int32_t *pos;
   const int64_t *turns;
   int64_t tokens;
-  int32_t half, offset, rot;
-  uint32_t rot_units;     // half / V
-  uint32_t token_units;   // both tensors
-  uint32_t unit_span;     // units of a token that one CTA does (grid.y parts)
+  int32_t offset, rot;
+  FastDiv half;
+  uint32_t rot_units;   // of a head
+  uint32_t token_units; // both tensors
+  FastDiv span;         // units of a token that one CTA does (grid.y parts)
+  int32_t abreast;      // tokens side by side in a CTA
   int32_t tokens_per_cta;
-  int32_t interleaved;
   float amplitude, sign;
+};
+// Vectors, pairs and tokens in flight of a thread: neighbours that turn together lie in one vector,
+// halves that do in two.
+template <class T, int V, bool I>
+struct RotShape {
+  static constexpr int vecs = I && V > 1 ? 1 : 2;
+  static constexpr int pairs = I && V > 1 ? V / 2 : V;
+  static constexpr int batch = V == 1 ? 4 : 128 / (vecs * V * static_cast<int>(sizeof(T))) > 8 ? 8 : 128 / (vecs * V * static_cast<int>(sizeof(T)));
 };
 
 // ---------------------------------------------------------------------------
-// rotary_kernel<T, V>: a unit is V pairs of one head (2V values), or V values
-// outside the rotated part, which are only copied.  A CTA does the units of
-// tokens_per_cta tokens (or a part of one token's, grid.y); the cosines and
-// sines of its tokens are computed once into shared memory and serve every
-// head of q and k.  The work is one read and one write of the tensors; the
-// instructions per unit (two divisions by multiplication, 4 FMA a pair) stay
-// below what hides under them.
+// rotary_kernel<T, V, I>: a unit is V values of one head and their partners (for interleaved
+// pairs these are among them), or V values outside the rotated part, which are only copied.
+// A thread keeps its unit (which tensor, head and pairs) for `batch` tokens; all its loads are under
+// way before the cosines and sines of the CTA's tokens are computed, once into shared
+// memory for every head of q and k.  Bound by one read and one write of the tensors: 8191 tokens of
+// 32 + 8 heads of 128 (168 MB) take 26 us, 6.4 TB/s; with the loads behind the sines 44 us.
 // ---------------------------------------------------------------------------
-template <class T, int V>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotArgs a) {
-  extern __shared__ float2 cs[];  // [tokens_per_cta][half]
+template <class T, int V, bool I>
+__global__ void __launch_bounds__(kRotThreads, 2) rotary_kernel(const RotArgs a) {
+  using Sh = RotShape<T, V, I>;
+  extern __shared__ __align__(16) float2 cs[];
   pdl_wait();
   pdl_launch();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens_per_cta;
   const int nt = static_cast<int>(min(static_cast<int64_t>(a.tokens_per_cta), a.tokens - t0));
-  for (int i = threadIdx.x; i < nt * a.half; i += kRotThreads) {
-    const int t = i / a.half, p = i - t * a.half;
-    cs[i] = rotary_cos_sin(a.pos[t0 + t], a.turns[p], a.amplitude, a.sign);
+  uint32_t lane_t, u;  // which of the tokens abreast; the unit of the token
+  a.span.divmod(threadIdx.x, lane_t, u);
+  u += blockIdx.y * a.span.d;
+  const bool mine = lane_t < static_cast<uint32_t>(a.abreast) && u < a.token_units;
+  const int which = u >= a.t[0].per_token;
+  const RotTensor &x = a.t[which];
+  if (which) u -= a.t[0].per_token;
+  uint32_t head, unit;
+  x.units.divmod(u, head, unit);
+  const bool rotates = unit < a.rot_units;
+  const int far = I ? 1 : a.rot / 2;
+  int d;
+  if (rotates) {
+    d = a.offset + static_cast<int>(unit) * (I ? 2 * Sh::pairs : V);
+  } else {
+    d = static_cast<int>(unit - a.rot_units) * V;
+    if (d >= a.offset) d += a.rot;
+  }
+  using Vt = Vec<T, V>;
+  Vt lo[Sh::batch], hi[Sh::vecs == 2 ? Sh::batch : 1];
+  const T *src = static_cast<const T *>(x.x) + (t0 + lane_t) * x.xt + head * x.xh + d;
+  const int64_t xs = a.abreast * x.xt;
+#pragma unroll
+  for (int b = 0; b < Sh::batch; ++b)
+    if (mine && lane_t + b * a.abreast < nt) {
+      lo[b] = *reinterpret_cast<const Vt *>(src + b * xs);
+      if (Sh::vecs == 2 && rotates) hi[Sh::vecs == 2 ? b : 0] = *reinterpret_cast<const Vt *>(src + b * xs + far);
+    }
+  const int half = a.half.d;
+  for (uint32_t i = threadIdx.x; i < nt * half; i += blockDim.x) {
+    uint32_t t, p;
+    a.half.divmod(i, t, p);
+    cs[table_at<Sh::pairs>(p, t, nt, a.rot_units)] =
+        rotary_cos_sin(a.pos[t0 + t], a.turns[p], a.amplitude, a.sign);
   }
   __syncthreads();
-  const uint32_t u0 = blockIdx.y * a.unit_span;
-  const uint32_t span = min(a.unit_span, a.token_units - u0);
-  const uint32_t total = span * nt;
-  for (uint32_t base = threadIdx.x; base < total; base += kRotThreads * kRotBatch) {
-    float lo[kRotBatch][V], hi[kRotBatch][V];
-    T *out[kRotBatch];
-    int cs_at[kRotBatch];  // -1: copied, -2: nothing
+  if (!mine) return;
+  T *dst = static_cast<T *>(x.y) + (t0 + lane_t) * x.yt + head * x.yh + d;
+  const int64_t ys = a.abreast * x.yt;
 #pragma unroll
-    for (int j = 0; j < kRotBatch; ++j) {
-      uint32_t i = base + j * kRotThreads;
-      cs_at[j] = -2;
-      if (i >= total) continue;
-      uint32_t tok = 0;
-      if (nt > 1) {
-        tok = i / span;
-        i -= tok * span;
-      }
-      uint32_t u = u0 + i;
-      const int which = u >= a.t[0].per_token;
-      const RotTensor &x = a.t[which];
-      if (which) u -= a.t[0].per_token;
-      uint32_t head, unit;
-      x.units.divmod(u, head, unit);
-      const T *src = static_cast<const T *>(x.x) + (t0 + tok) * x.xt + head * x.xh;
-      T *dst = static_cast<T *>(x.y) + (t0 + tok) * x.yt + head * x.yh;
-      if (unit < a.rot_units) {
-        const int p = unit * V;
-        cs_at[j] = static_cast<int>(tok) * a.half + p;
-        const int d = a.offset + (a.interleaved ? 2 * p : p);
-        out[j] = dst + d;
-        load_vec<T, V>(src + d, lo[j]);
-        load_vec<T, V>(src + d + (a.interleaved ? V : a.half), hi[j]);
-      } else {
-        int d = static_cast<int>(unit - a.rot_units) * V;
-        if (d >= a.offset) d += a.rot;
-        cs_at[j] = -1;
-        out[j] = dst + d;
-        load_vec<T, V>(src + d, lo[j]);
-      }
-    }
+  for (int b = 0; b < Sh::batch; ++b) {
+    const int t = lane_t + b * a.abreast;
+    if (t >= nt) break;
+    Vt na = lo[b];
+    if (rotates) {
+      float2 w[Sh::pairs];
+      table_read<Sh::pairs>(cs, unit, t, nt, a.rot_units, w);
+      if constexpr (V == 1) {
+        Vt nb;
+        const float p = to_f32<T>(lo[b].e), q = to_f32<T>(hi[b].e);
+        na.e = from_f32<T>(p * w[0].x - q * w[0].y);
+        nb.e = from_f32<T>(p * w[0].y + q * w[0].x);
+        *reinterpret_cast<Vt *>(dst + b * ys + far) = nb;
+      } else if constexpr (Sh::vecs == 1) {
 #pragma unroll
-    for (int j = 0; j < kRotBatch; ++j) {
-      if (cs_at[j] == -2) continue;
-      if (cs_at[j] >= 0) {
-        float na[V], nb[V];
-        const float2 *c = cs + cs_at[j];
-        if (a.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 2 * V; i += 2) {  // pair i/2 of the 2V values [lo | hi]
-            const float x = i < V ? lo[j][i % V] : hi[j][i % V];
-            const float y = i + 1 < V ? lo[j][(i + 1) % V] : hi[j][(i + 1) % V];
-            const float2 w = c[i / 2];
-            const float r0 = x * w.x - y * w.y, r1 = x * w.y + y * w.x;
-            if (i < V) na[i % V] = r0; else nb[i % V] = r0;
-            if (i + 1 < V) na[(i + 1) % V] = r1; else nb[(i + 1) % V] = r1;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float2 w = c[i];
-            na[i] = lo[j][i] * w.x - hi[j][i] * w.y;
-            nb[i] = lo[j][i] * w.y + hi[j][i] * w.x;
-          }
+        for (int i = 0; i < Sh::pairs; ++i) {
+          const float2 p = lo[b].pair(i);
+          na.set_pair(i, p.x * w[i].x - p.y * w[i].y, p.x * w[i].y + p.y * w[i].x);
         }
-        store_vec<T, V>(out[j], na);
-        store_vec<T, V>(out[j] + (a.interleaved ? V : a.half), nb);
       } else {
-        store_vec<T, V>(out[j], lo[j]);
+        Vt nb;
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+          const float2 p = lo[b].pair(i / 2), q = hi[b].pair(i / 2);
+          na.set_pair(i / 2, p.x * w[i].x - q.x * w[i].y, p.y * w[i + 1].x - q.y * w[i + 1].y);
+          nb.set_pair(i / 2, p.x * w[i].y + q.x * w[i].x, p.y * w[i + 1].y + q.y * w[i + 1].x);
+        }
+        *reinterpret_cast<Vt *>(dst + b * ys + far) = nb;
       }
     }
+    *reinterpret_cast<Vt *>(dst + b * ys) = na;
   }
 }
 
-template <class T, int V>
-int launch_rotary(const hisparse_rotary_args &g, bool copies, void *stream) {
+template <class T, int V, bool I>
+int launch_rotary(const hisparse_rotary_args &g, void *stream) {
+  using Sh = RotShape<T, V, I>;
   RotArgs a = {};
   a.pos = g.d_positions;
   a.turns = g.d_turns;
   a.tokens = g.tokens;
   a.rot = g.rot_dim;
-  a.half = g.rot_dim / 2;
+  a.half = FastDiv(g.rot_dim / 2);
   a.offset = g.offset;
-  a.rot_units = a.half / V;
-  a.interleaved = (g.flags & HISPARSE_ROTARY_INTERLEAVED) != 0;
+  a.rot_units = g.rot_dim / 2 / Sh::pairs;
   a.amplitude = g.amplitude;
   a.sign = (g.flags & HISPARSE_ROTARY_INVERSE) ? -1.f : 1.f;
   for (int j = 0; j < 2; ++j) {
@@ -143,29 +172,28 @@ int launch_rotary(const hisparse_rotary_args &g, bool copies, void *stream) {
       a.t[j].units = FastDiv(1);
       continue;
     }
-    const uint32_t per = a.rot_units + (copies && t.x != t.y ? (t.dim - g.rot_dim) / V : 0);
+    const uint32_t per = a.rot_units + (t.x != t.y ? (t.dim - g.rot_dim) / V : 0);
     a.t[j] = {t.x, t.y, t.x_token_stride, t.x_head_stride, t.y_token_stride, t.y_head_stride,
               FastDiv(per), per * static_cast<uint32_t>(t.heads)};
     a.token_units += a.t[j].per_token;
   }
-  // About two batches of units a thread; few tokens are split over several CTAs.
-  const uint32_t want = kRotThreads * kRotBatch * 2;
-  const int64_t all = static_cast<int64_t>(a.token_units) * g.tokens;
-  const uint32_t share = static_cast<uint32_t>(
-      std::min<int64_t>(want, std::max<int64_t>(kRotThreads, all / 304)));
-  const int max_tokens = std::max(1, 32768 / (a.half * 8));  // 32 KB of cosines and sines
-  a.tokens_per_cta = std::min<int64_t>(
-      std::min<int64_t>(max_tokens, g.tokens), std::max<uint32_t>(1, share / a.token_units));
-  uint32_t parts = (a.token_units + share - 1) / share;
-  if (a.tokens_per_cta > 1) parts = 1;
-  parts = std::min<uint32_t>(parts, 65535);
-  a.unit_span = (a.token_units + parts - 1) / parts;
-  parts = (a.token_units + a.unit_span - 1) / a.unit_span;
+  // A token's units over CTAs of nearly equal share; several tokens abreast where they are few.
+  uint32_t parts = (a.token_units + kRotThreads - 1) / kRotThreads;
+  const uint32_t span = (a.token_units + parts - 1) / parts;
+  parts = (a.token_units + span - 1) / span;
+  if (parts > 65535) return HISPARSE_EBOUND;
+  a.span = FastDiv(span);
+  const int64_t row = static_cast<int64_t>(g.rot_dim) / 2 * static_cast<int>(sizeof(float2));
+  const int64_t fit = std::max<int64_t>(1, kRotTable / row);  // (rot_dim is at most 8192: 32 KB)
+  a.abreast = static_cast<int>(std::min<int64_t>({kRotThreads / span, g.tokens, fit}));
+  // Tokens in a row: enough to have `batch` loads in flight, unless SMs would be left without.
+  const int64_t turns = std::max<int64_t>(1, std::min<int64_t>(Sh::batch, g.tokens * parts / (a.abreast * 304)));
+  a.tokens_per_cta = static_cast<int>(std::min({turns * a.abreast, fit, g.tokens}));
   const int64_t gx = (g.tokens + a.tokens_per_cta - 1) / a.tokens_per_cta;
   if (gx > 0x7fffffff) return HISPARSE_EBOUND;
-  const size_t smem = static_cast<size_t>(a.tokens_per_cta) * a.half * sizeof(float2);
-  return launch_pdl(rotary_kernel<T, V>, dim3(static_cast<unsigned>(gx), parts), dim3(kRotThreads),
-                    smem, stream, 1, a);
+  const int threads = (a.abreast * static_cast<int>(span) + 31) / 32 * 32;
+  return launch_pdl(rotary_kernel<T, V, I>, dim3(static_cast<unsigned>(gx), parts), dim3(threads),
+                    a.tokens_per_cta * row, stream, 1, a);
 }
 
 template <class T>
@@ -186,35 +214,45 @@ int pick_rotary(const hisparse_rotary_args &g, void *stream) {
     }
     return true;
   };
-  if (fits(8)) return launch_rotary<T, 8>(g, true, stream);
-  if (fits(4)) return launch_rotary<T, 4>(g, true, stream);
-  return launch_rotary<T, 1>(g, true, stream);
+  const bool i = (g.flags & HISPARSE_ROTARY_INTERLEAVED) != 0;
+  if (fits(8)) return i ? launch_rotary<T, 8, true>(g, stream) : launch_rotary<T, 8, false>(g, stream);
+  if (fits(4)) return i ? launch_rotary<T, 4, true>(g, stream) : launch_rotary<T, 4, false>(g, stream);
+  return i ? launch_rotary<T, 1, true>(g, stream) : launch_rotary<T, 1, false>(g, stream);
 }
 
 // ---------------------------------------------------------------------------
 // Packing
 // ---------------------------------------------------------------------------
-constexpr int kPackThreads = 256;
-constexpr int kPackTable = 48 * 1024;  // bytes of cosines and sines a CTA may hold
+constexpr int kLow = 8;  // tokens of the low table of angles
 
+struct PackSide {
+  const void *x;
+  int64_t ts, hs;  // elements between tokens, heads
+  int32_t dim, row_at;
+  FastDiv upt;     // units of 16 values in a token's head
+  int32_t abreast; // tokens side by side in a team
+};
 struct PackArgs {
+  PackSide side[2];
   const int32_t *cu, *start, *reqs;
-  const void *k, *v;
-  int64_t tokens, kt, kh, vt, vh;
+  int64_t tokens;
   float *scales;
   int64_t scales_req;
   int32_t n, max_len, R, scale_blocks, S;
-  int32_t kv_heads, k_dim, v_dim, columns, cols_per_cta;
+  int32_t kv_heads, columns;
+  int32_t team;                // threads to a block's head: a power of two, or whole warps
+  int32_t heads, blocks_cta;   // teams of a CTA: heads of each of its blocks
+  int32_t k_groups;            // CTAs for the K heads
   float headroom;
   char *dst;
   int64_t dst_rows, dst_row, dst_req;
-  const int32_t *blocks;
+  const int32_t *pages;
   int32_t max_blocks, page_tokens;
-  int32_t rot, half, rot_offset, interleaved;
+  int32_t rot, rot_offset, interleaved;
+  FastDiv half;
   float amplitude, sign;
   const int64_t *turns;
   uint32_t *status;
-  int32_t chunk_k, chunk_v;  // tokens whose values a CTA's registers hold
 };
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -222,219 +260,255 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float inv) {
-  uint2 r;
-  r.x = e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
-  r.y = e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16;
-  return r;
-}
-__device__ __forceinline__ float finite_max(float m, float x) {
-  x = fabsf(x);
-  return x < INFINITY ? fmaxf(m, x) : m;
-}
-
-// Unit u of a head: two runs of 8 values, at d0 and d1.  The first rot / 16 units are
-// the rotating ones; the rest walk the values outside the rotated part.
-struct Unit {
-  int d0, d1, pair;  // pair: first of its 8 pairs, -1: not rotated
-};
-__device__ __forceinline__ Unit unit_at(const PackArgs &a, int u, bool rotates) {
-  Unit r;
-  const int ru = rotates ? a.rot >> 4 : 0;
-  if (u < ru) {
-    r.pair = u * 8;
-    r.d0 = a.rot_offset + (a.interleaved ? 16 * u : 8 * u);
-    r.d1 = r.d0 + (a.interleaved ? 8 : a.half);
-  } else {
-    r.pair = -1;
-    const int e = (u - ru) * 16;
-    r.d0 = rotates && e >= a.rot_offset ? e + a.rot : e;
-    r.d1 = rotates && e + 8 >= a.rot_offset ? e + 8 + a.rot : e + 8;
-  }
-  return r;
+__device__ __forceinline__ float2 turned(float2 a, float2 b) {  // a * b as complex numbers
+  return make_float2(a.x * b.x - a.y * b.y, a.x * b.y + a.y * b.x);
 }
 
 // ---------------------------------------------------------------------------
-// pack_kernel<T, PU>: one CTA per (block of the sequence, sequence, group of
-// heads).  For each head it reads the block's tokens once into registers (PU units
-// of 16 values a thread), rotates them, reduces their largest magnitude over
-// the CTA, fixes the scale, and writes the e4m3 bytes.  Blocks with more
-// tokens than the registers hold are walked twice in chunks (the second
-// read comes from L2).  The cosines and sines of the tokens are computed once
-// into shared memory and serve all heads of the CTA.  Bound by its bytes:
-// 2 (or 4) read and 1 written a value.
+// pack_kernel<T, PU, THREADS, WALK>: one CTA per (block of the sequence or several small ones,
+// sequence, group of heads), a team of threads to a head of a block.  A unit is two runs of 8 values: partners of a rotation, or
+// two stretches that are only packed.  A thread keeps its unit for PU tokens of the block:
+// it reads them, turns them, holds them in 32 bits, and once the largest magnitude of the head is
+// known writes their e4m3 bytes.  Blocks with more tokens than the CTA's registers hold are
+// walked twice (WALK; the second read comes from L2).
+// A token's angle is the sum of one of 8 low tokens' and one of the eighths': nt / 8 + 8 sines a pair
+// in place of nt, and the product of the two costs a thread 4 multiplies a pair (one more rounding of
+// 32 bits than the sine's own).
+// Its bytes, 2 (or 4) read and 1 written a value, would allow half the time; what binds is the
+// instructions (about 20 a value, 2.6 issued a cycle) and the wait of each CTA for its one round of
+// loads.  8 ragged prompts of up to 4096 tokens, 8 + 8 heads of 128 (151 MB) take 45 us, 3.4 TB/s: with
+// 4 units a thread and 3 CTAs of 256 threads to an SM (80 registers); 2 units and 2 CTAs of 512 took
+// 53, 1 unit 79, 4 units and 6 CTAs of 128 49.  A sine for every token and pair, and the rotation
+// done twice in place of held, took 105.
 // ---------------------------------------------------------------------------
-template <class T, int PU>
-__global__ void __launch_bounds__(kPackThreads) pack_kernel(const PackArgs a) {
-  extern __shared__ float2 cs[];  // [chunk_k][half]
-  __shared__ float s_max[kPackThreads / 32];
-  __shared__ float s_scale;
+template <class T, int PU, int THREADS, bool WALK>
+__global__ void __launch_bounds__(THREADS, 768 / THREADS) pack_kernel(const PackArgs a) {
+  extern __shared__ __align__(16) float2 angles[];  // low: kLow tokens, then one for each kLow of a chunk
+  __shared__ uint32_t s_max[20];
   pdl_wait();
   pdl_launch();
-  const int seq = blockIdx.y, tid = threadIdx.x;
+  const int seq = blockIdx.y;
   const int64_t cu0 = a.cu ? a.cu[seq] : static_cast<int64_t>(seq) * a.max_len;
   const int64_t len = (a.cu ? a.cu[seq + 1] : cu0 + a.max_len) - cu0;
-  const int64_t p0 = a.start[seq];
+  const int32_t p0 = a.start[seq];
   const int req = a.reqs ? a.reqs[seq] : seq;
   if (len <= 0) return;
-  if (len > a.max_len || cu0 < 0 || cu0 + len > a.tokens || p0 < 0 || req < 0 || req >= a.R) {
-    if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0 && a.status)
+  if (len > a.max_len || cu0 < 0 || cu0 + len > a.tokens || p0 < 0 || len > INT32_MAX - p0 || req < 0 ||
+      req >= a.R) {
+    if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0 && a.status)
       atomicOr(a.status, HISPARSE_ERR_RANGE);
     return;
   }
-  const int64_t blk = p0 / a.S + blockIdx.x;
-  const int64_t first = max(blk * a.S, p0), end = min(blk * a.S + a.S, p0 + len);
-  if (first >= end) return;
-  if (blk >= a.scale_blocks) {
+  // The CTA's blocks and tokens, then this thread's team's.
+  const uint32_t blk0 = static_cast<uint32_t>(p0) / a.S + blockIdx.x * a.blocks_cta;
+  const int64_t stop = p0 + len;
+  const int64_t cta_base = static_cast<int64_t>(blk0) * a.S;
+  const int64_t cta_first = max(cta_base, static_cast<int64_t>(p0));
+  if (cta_first >= stop) return;
+  const int cta_tokens = static_cast<int>(min(cta_base + static_cast<int64_t>(a.blocks_cta) * a.S, stop) - cta_first);
+  const int team = threadIdx.x / a.team, tid = threadIdx.x - team * a.team;
+  const int group = team / a.heads;
+  const bool is_v = static_cast<int>(blockIdx.z) >= a.k_groups;
+  const int head = (is_v ? blockIdx.z - a.k_groups : blockIdx.z) * a.heads + (team - group * a.heads);
+  const uint32_t blk = blk0 + group;
+  const int64_t base = cta_base + static_cast<int64_t>(group) * a.S;
+  const int32_t first = static_cast<int32_t>(min(max(base, cta_first), stop));
+  int nt = group < a.blocks_cta ? static_cast<int>(min(base + a.S, stop) - first) : 0;
+  const bool has_first = first == base, has_last = nt > 0 && first + static_cast<int64_t>(nt) == base + a.S;
+  if (nt > 0 && blk >= static_cast<uint32_t>(a.scale_blocks)) {
     if (tid == 0 && a.status) atomicOr(a.status, HISPARSE_ERR_RANGE);
-    return;
+    nt = 0;
   }
-  const int nt = static_cast<int>(end - first);
   const int64_t tok0 = cu0 + (first - p0);  // the call's token of position `first`
-  const bool has_first = first == blk * a.S, has_last = end == blk * a.S + a.S;
+  const int off = static_cast<int>(first - cta_first);
 
-  const int col_end = min(a.columns, static_cast<int>(blockIdx.z + 1) * a.cols_per_cta);
-  int table_at = -1;  // first token of the chunk whose table is in shared memory
-  for (int col = blockIdx.z * a.cols_per_cta; col < col_end; ++col) {
-    const bool is_k = col < a.kv_heads;
-    const int head = is_k ? col : col - a.kv_heads;
-    const int dim = is_k ? a.k_dim : a.v_dim;
-    const int upt = dim >> 4;
-    const int chunk = is_k ? a.chunk_k : a.chunk_v;
-    const bool rot = is_k && a.rot > 0;
-    const T *src = static_cast<const T *>(is_k ? a.k : a.v) + head * (is_k ? a.kh : a.vh);
-    const int64_t ts = is_k ? a.kt : a.vt;
-    const int64_t row_at = is_k ? static_cast<int64_t>(head) * a.k_dim
-                                : static_cast<int64_t>(a.kv_heads) * a.k_dim +
-                                      static_cast<int64_t>(head) * a.v_dim;
-    float *scale_p = a.scales + req * a.scales_req + blk * a.columns + col;
+  // this thread's tokens and unit; a CTA has K heads or V heads
+  const PackSide &sd = a.side[is_v];
+  uint32_t lane_t, unit;
+  sd.upt.divmod(tid, lane_t, unit);
+  const bool mine = nt > 0 && head < a.kv_heads && lane_t < static_cast<uint32_t>(sd.abreast);
+  const bool rot = !is_v && a.rot > 0;
+  const int half = a.half.d, units = half >> 3;  // rotating units
+  const bool turns = rot && unit < static_cast<uint32_t>(units);
+  int d0, d1;
+  if (turns) {
+    d0 = a.rot_offset + (a.interleaved ? 16 : 8) * static_cast<int>(unit);
+    d1 = d0 + (a.interleaved ? 8 : half);
+  } else {
+    const int skip = rot ? a.rot : 0;
+    d0 = 8 * static_cast<int>(rot ? unit - units : unit);
+    d1 = d0 + (sd.dim - skip) / 2;
+    if (rot && d0 >= a.rot_offset) d0 += skip;
+    if (rot && d1 >= a.rot_offset) d1 += skip;
+  }
+  const T *src = static_cast<const T *>(sd.x) + (tok0 + lane_t) * sd.ts + head * sd.hs;
+  float *scale_p = a.scales + req * a.scales_req + static_cast<int64_t>(blk) * a.columns + (is_v ? a.kv_heads + head : head);
+  const float old = mine ? *scale_p : 0.f;
+  const int chunk = sd.abreast * PU, chunks = WALK ? (cta_tokens + chunk - 1) / chunk : 1;
+  float2 *const low = angles, *const high = angles + kLow * half;
+  using Vt = Vec<T, 8>;
+  float m = 0.f, inv = 0.f;
+  if (threadIdx.x < 20) s_max[threadIdx.x] = 0;
+
+  for (int step = 0; step < (chunks == 1 ? 1 : 2 * chunks); ++step) {
+    const int c0 = WALK ? (step < chunks ? step : step - chunks) * chunk : 0;
+    Vt raw[PU][2];
+#pragma unroll
+    for (int j = 0; j < PU; ++j) {
+      const int t = c0 + lane_t + j * sd.abreast;
+      if (mine && t < nt) {
+        const T *p = src + static_cast<int64_t>(c0 + j * sd.abreast) * sd.ts;
+        raw[j][0] = *reinterpret_cast<const Vt *>(p + d0);
+        raw[j][1] = *reinterpret_cast<const Vt *>(p + d1);
+      } else {
+        raw[j][0] = raw[j][1] = Vt{};
+      }
+    }
+    const int n_table = WALK ? min(chunk, cta_tokens - c0) : cta_tokens;
+    const int n_high = (n_table + kLow - 1) / kLow;
+    if (rot) {
+      if (step) __syncthreads();
+      const int n_low = min(kLow, n_table);
+      for (uint32_t i = threadIdx.x; i < (n_low + n_high) * half; i += blockDim.x) {
+        uint32_t t, p;
+        a.half.divmod(i, t, p);
+        const bool lo = t < n_low;
+        if (!lo) t -= n_low;
+        const float2 w = rotary_cos_sin(lo ? static_cast<uint32_t>(cta_first) + c0 + t : t * kLow, a.turns[p], lo ? a.amplitude : 1.f, a.sign);
+        (lo ? low : high)[table_at<8>(p, t, lo ? kLow : n_high, units)] = w;
+      }
+    }
+    __syncthreads();
     float x[PU][16];
-    auto fetch = [&](int c0, int cn) {
-      if (rot && table_at != c0) {
-        __syncthreads();
-        for (int i = tid; i < cn * a.half; i += kPackThreads) {
-          const int t = i / a.half, p = i - t * a.half;
-          cs[i] = rotary_cos_sin(static_cast<int32_t>(first + c0 + t), a.turns[p], a.amplitude,
-                                 a.sign);
-        }
-        table_at = c0;
-        __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PU; ++j) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float2 p = raw[j][e >> 3].pair((e & 7) / 2);
+        x[j][e] = p.x;
+        x[j][e + 1] = p.y;
       }
+      const int t = off + lane_t + j * sd.abreast;
+      if (turns && t - off + c0 < nt) {
 #pragma unroll
-      for (int j = 0; j < PU; ++j) {
-        const int i = tid + j * kPackThreads;
-        if (i < cn * upt) {
-          const int t = i / upt;
-          const Unit u = unit_at(a, i - t * upt, rot);
-          const T *p = src + (tok0 + c0 + t) * ts;
-          load_vec<T, 8>(p + u.d0, *reinterpret_cast<float(*)[8]>(&x[j][0]));
-          load_vec<T, 8>(p + u.d1, *reinterpret_cast<float(*)[8]>(&x[j][8]));
-        }
-      }
-      if (!rot) return;
+        for (int e = 0; e < 8; e += 2) {
+          const float4 l = *reinterpret_cast<const float4 *>(low + ((e >> 1) * kLow + (t & (kLow - 1))) * 2 * units + 2 * unit);
+          const float4 h = *reinterpret_cast<const float4 *>(high + ((e >> 1) * n_high + t / kLow) * 2 * units + 2 * unit);
+          const float2 w[2] = {turned(make_float2(l.x, l.y), make_float2(h.x, h.y)),
+                               turned(make_float2(l.z, l.w), make_float2(h.z, h.w))};
 #pragma unroll
-      for (int j = 0; j < PU; ++j) {
-        const int i = tid + j * kPackThreads;
-        if (i >= cn * upt) continue;
-        const int t = i / upt;
-        const Unit u = unit_at(a, i - t * upt, rot);
-        if (u.pair < 0) continue;
-        const float2 *c = cs + t * a.half + u.pair;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 w = c[e];
-          float &p = a.interleaved ? x[j][2 * e] : x[j][e];
-          float &q = a.interleaved ? x[j][2 * e + 1] : x[j][8 + e];
-          const float np = p * w.x - q * w.y;
-          q = p * w.y + q * w.x;
-          p = np;
+          for (int i = 0; i < 2; ++i) {
+            float &p = a.interleaved ? x[j][2 * (e + i)] : x[j][e + i];
+            float &q = a.interleaved ? x[j][2 * (e + i) + 1] : x[j][8 + e + i];
+            const float np = p * w[i].x - q * w[i].y;
+            q = p * w[i].y + q * w[i].x;
+            p = np;
+          }
         }
       }
-    };
-    float m = 0.f;
-    const float old = *scale_p;
-    const bool fresh = has_first || old == 0.f;
-    for (int c0 = 0; c0 < nt; c0 += chunk) {
-      const int cn = min(chunk, nt - c0);
-      if (!fresh && nt > chunk) break;  // the scale stands and the values are read below
-      fetch(c0, cn);
+    }
+    if (step < chunks) {
+      // The largest finite magnitude.  fmaxf leaves NaN out; infinities are rare, and looked for only
+      // where the plain maximum is one.
+      float top = 0.f;
 #pragma unroll
       for (int j = 0; j < PU; ++j)
-        if (tid + j * kPackThreads < cn * upt) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) m = finite_max(m, x[j][e]);
-        }
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[j][e]));
+      if (top == INFINITY) {
+        top = 0.f;
+#pragma unroll
+        for (int j = 0; j < PU; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float y = fabsf(x[j][e]);
+            top = fmaxf(top, y < INFINITY ? y : 0.f);
+          }
+      }
+      m = fmaxf(m, top);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    __syncthreads();  // every thread has read `old`, and s_max and s_scale are free
-    if ((tid & 31) == 0) s_max[tid >> 5] = m;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 0; w < kPackThreads / 32; ++w) m = fmaxf(m, s_max[w]);
+    if (step == chunks - 1) {
+      // Magnitudes are not negative: their bits compare as they do.
+      uint32_t w = __float_as_uint(m);
+      if (a.team >= 32) {
+        w = __reduce_max_sync(0xffffffffu, w);
+        if ((threadIdx.x & 31) == 0) atomicMax(&s_max[team], w);
+        __syncthreads();  // (every thread has read `old`)
+        w = s_max[team];
+      } else {
+        for (int o = a.team >> 1; o; o >>= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
+        __syncwarp();
+      }
+      m = __uint_as_float(w);
       float s = old;
-      if (fresh && m > 0.f) {
+      if ((has_first || old == 0.f) && m > 0.f) {
         s = fmaxf(m * ((has_last ? 1.f : a.headroom) / 448.f), 0x1p-100f);
-        *scale_p = s;
+        if (tid == 0 && mine) *scale_p = s;
       }
-      s_scale = s;
+      inv = s > 0.f ? 1.f / s : 0.f;
     }
-    __syncthreads();
-    const float inv = s_scale > 0.f ? 1.f / s_scale : 0.f;
-    for (int c0 = 0; c0 < nt; c0 += chunk) {
-      const int cn = min(chunk, nt - c0);
-      if (nt > chunk) fetch(c0, cn);
+    if (step < chunks && chunks > 1) continue;
 #pragma unroll
-      for (int j = 0; j < PU; ++j) {
-        const int i = tid + j * kPackThreads;
-        if (i >= cn * upt) continue;
-        const int t = i / upt;
-        const Unit u = unit_at(a, i - t * upt, rot);
-        const int64_t pos = first + c0 + t;
-        int64_t row = a.dst_req ? pos : tok0 + c0 + t;
-        if (a.blocks) {
-          const int64_t b = pos / a.page_tokens;
-          const int32_t page = b < a.max_blocks
-                                   ? a.blocks[static_cast<int64_t>(req) * a.max_blocks + b]
-                                   : -1;
-          if (page == -1) continue;  // no resident copy of this token
-          row = static_cast<int64_t>(page) * a.page_tokens + pos % a.page_tokens;
-        }
-        if (row < 0 || row >= a.dst_rows) {
-          if (a.status) atomicOr(a.status, HISPARSE_ERR_RANGE);
-          continue;
-        }
-        char *out = a.dst + req * a.dst_req + row * a.dst_row + row_at;
-        *reinterpret_cast<uint2 *>(out + u.d0) =
-            e4m3x8(*reinterpret_cast<float(*)[8]>(&x[j][0]), inv);
-        *reinterpret_cast<uint2 *>(out + u.d1) =
-            e4m3x8(*reinterpret_cast<float(*)[8]>(&x[j][8]), inv);
+    for (int j = 0; j < PU; ++j) {
+      const int t = c0 + lane_t + j * sd.abreast;
+      if (!mine || t >= nt) break;
+      int64_t row = a.dst_req ? first + t : tok0 + t;
+      if (a.pages) {
+        const uint32_t pos = first + t, b = pos / a.page_tokens;
+        const int32_t page = b < static_cast<uint32_t>(a.max_blocks) ? a.pages[static_cast<int64_t>(req) * a.max_blocks + b] : -1;
+        if (page == -1) continue;  // no resident copy of this token
+        row = static_cast<int64_t>(page) * a.page_tokens + (pos - b * a.page_tokens);
       }
+      if (row < 0 || row >= a.dst_rows) {
+        if (a.status) atomicOr(a.status, HISPARSE_ERR_RANGE);
+        continue;
+      }
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = e4m3x2(x[j][4 * e] * inv, x[j][4 * e + 1] * inv) | e4m3x2(x[j][4 * e + 2] * inv, x[j][4 * e + 3] * inv) << 16;
+      char *out = a.dst + req * a.dst_req + row * a.dst_row + sd.row_at + head * sd.dim;
+      *reinterpret_cast<uint2 *>(out + d0) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2 *>(out + d1) = make_uint2(w[2], w[3]);
     }
   }
 }
 
-template <class T, int PU>
-int launch_pack(PackArgs a, int span, int groups, void *stream) {
-  const int cap = kPackThreads * PU;
-  a.chunk_k = std::max(1, cap / (a.k_dim / 16));
-  a.chunk_v = std::max(1, cap / (a.v_dim / 16));
-  int table = 0;
-  if (a.rot) {
-    a.chunk_k = std::min(a.chunk_k, kPackTable / (a.half * 8));
-    table = std::min({a.chunk_k, a.S, a.max_len}) * a.half * 8;
+template <class T, int PU, int THREADS, bool WALK>
+int launch_pack(PackArgs a, int span, int most, void *stream) {
+  // Tokens abreast so that a team holds a block's tokens, within a CTA; then heads to a CTA (they
+  // share the angles), then blocks, while there are CTAs for every SM.
+  const int sides = a.columns > a.kv_heads ? 2 : 1;
+  const int upt = std::max(a.side[0].dim, sides > 1 ? a.side[1].dim : 0) / 16;
+  const int want = upt * ((most + PU - 1) / PU);
+  a.team = std::min(THREADS, (want + 31) / 32 * 32);
+  if (want < 32)
+    for (a.team = 1; a.team < want;) a.team *= 2;
+  const int64_t all = static_cast<int64_t>(span) * a.n * a.columns;
+  const int teams = static_cast<int>(std::min<int64_t>(THREADS / a.team, std::max<int64_t>(1, all / 304)));
+  a.heads = std::min(teams, a.kv_heads);
+  a.blocks_cta = WALK ? 1 : std::min(teams / a.heads, span);
+  for (int i = 0; i < sides; ++i) {
+    a.side[i].upt = FastDiv(a.side[i].dim / 16);
+    a.side[i].abreast = std::min(a.team / (a.side[i].dim / 16), most);
   }
-  return launch_pdl(pack_kernel<T, PU>, dim3(span, a.n, groups), dim3(kPackThreads), table, stream,
-                    1, a);
+  const int tokens = a.blocks_cta > 1 ? std::min(a.blocks_cta * a.S, a.max_len) : std::min(a.side[0].abreast * PU, most);
+  const int table = a.rot ? (kLow + (tokens + kLow - 1) / kLow) * (a.rot / 2) * static_cast<int>(sizeof(float2)) : 0;
+  a.k_groups = (a.kv_heads + a.heads - 1) / a.heads;
+  return launch_pdl(pack_kernel<T, PU, THREADS, WALK>, dim3((span + a.blocks_cta - 1) / a.blocks_cta, a.n, a.k_groups * sides),
+                    dim3((a.team * a.heads * a.blocks_cta + 31) / 32 * 32), table, stream, 1, a);
 }
 
 template <class T>
-int pick_pack(const PackArgs &a, int span, int groups, void *stream) {
-  const int tokens = std::min(a.S, a.max_len);
-  const int units = tokens * std::max(a.k_dim, a.v_dim) / 16;
-  if (units <= kPackThreads) return launch_pack<T, 1>(a, span, groups, stream);
-  if (units <= kPackThreads * 2) return launch_pack<T, 2>(a, span, groups, stream);
-  return launch_pack<T, 5>(a, span, groups, stream);
+int pick_pack(const PackArgs &a, int span, void *stream) {
+  // Four units a thread where there is work for every SM, one where there is not (or a block has no
+  // four tokens); a CTA of 640 threads where 256 would have to walk a block twice.
+  const int most = std::min(a.S, a.max_len);
+  const int upt = std::max(a.side[0].dim, a.side[1].dim) / 16;
+  const int64_t all = static_cast<int64_t>(span) * a.n * a.columns * upt * most;
+  if (upt * most <= 256 && (most < 4 || all <= 304 * 256)) return launch_pack<T, 1, 256, false>(a, span, most, stream);
+  if (upt * ((most + 3) / 4) <= 256) return launch_pack<T, 4, 256, false>(a, span, most, stream);
+  return launch_pack<T, 4, 640, true>(a, span, most, stream);
 }
 
 }  // namespace
@@ -500,18 +574,19 @@ int hisparse_pack(const hisparse_pack_args *g, void *stream) {
   }
   PackArgs a = {};
   a.cu = g->d_cu_lens; a.start = g->d_start; a.reqs = g->d_reqs;
-  a.k = g->k; a.v = g->v; a.tokens = g->tokens;
-  a.kt = g->k_token_stride; a.kh = g->k_head_stride;
-  a.vt = g->v_token_stride; a.vh = g->v_head_stride;
+  a.tokens = g->tokens;
+  a.side[0] = {g->k, g->k_token_stride, g->k_head_stride, r.k_dim, 0};
+  if (!r.latent)
+    a.side[1] = {g->v, g->v_token_stride, g->v_head_stride, r.v_dim, r.kv_heads * r.k_dim};
   a.scales = g->scales; a.scales_req = g->scales_req_stride;
   a.n = g->n; a.max_len = g->max_len; a.R = g->num_requests; a.scale_blocks = g->scale_blocks;
   a.S = r.block_tokens;
-  a.kv_heads = r.kv_heads; a.k_dim = r.k_dim; a.v_dim = r.v_dim; a.columns = record_columns(r);
+  a.kv_heads = r.kv_heads; a.columns = record_columns(r);
   a.headroom = g->headroom;
   a.dst = static_cast<char *>(g->dst);
   a.dst_rows = g->dst_rows; a.dst_row = g->dst_row_stride; a.dst_req = g->dst_req_stride;
-  a.blocks = g->d_blocks; a.max_blocks = g->max_blocks; a.page_tokens = g->page_tokens;
-  a.rot = g->rot_dim; a.half = g->rot_dim / 2; a.rot_offset = g->rot_offset;
+  a.pages = g->d_blocks; a.max_blocks = g->max_blocks; a.page_tokens = g->page_tokens;
+  a.rot = g->rot_dim; a.half = FastDiv(std::max(1, g->rot_dim / 2)); a.rot_offset = g->rot_offset;
   a.interleaved = (g->rot_flags & HISPARSE_ROTARY_INTERLEAVED) != 0;
   a.sign = (g->rot_flags & HISPARSE_ROTARY_INVERSE) ? -1.f : 1.f;
   a.amplitude = g->amplitude;
@@ -519,17 +594,11 @@ int hisparse_pack(const hisparse_pack_args *g, void *stream) {
   a.status = g->d_status;
   // A sequence of max_len tokens touches at most this many blocks, whatever its start.
   const int64_t span = (static_cast<int64_t>(g->max_len) + a.S - 2) / a.S + 1;
-  // Heads share the rotation's table: as many to a CTA as still leave some
-  // CTAs for every SM.
-  const int64_t ctas = span * g->n;
-  a.cols_per_cta = static_cast<int>(std::min<int64_t>(
-      a.columns, std::max<int64_t>(1, ctas * a.columns / (152 * 8))));
-  const int groups = (a.columns + a.cols_per_cta - 1) / a.cols_per_cta;
   if (span > 0x7fffffff) return HISPARSE_EBOUND;
   switch (g->dtype) {
-    case HISPARSE_BF16: return pick_pack<__nv_bfloat16>(a, static_cast<int>(span), groups, stream);
-    case HISPARSE_F16: return pick_pack<__half>(a, static_cast<int>(span), groups, stream);
-    default: return pick_pack<float>(a, static_cast<int>(span), groups, stream);
+    case HISPARSE_BF16: return pick_pack<__nv_bfloat16>(a, static_cast<int>(span), stream);
+    case HISPARSE_F16: return pick_pack<__half>(a, static_cast<int>(span), stream);
+    default: return pick_pack<float>(a, static_cast<int>(span), stream);
   }
 }
 
