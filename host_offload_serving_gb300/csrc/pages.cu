@@ -66,13 +66,14 @@ __device__ __forceinline__ int block_scan(int v, int *warp_sums, int &total) {
   return before + x - v;
 }
 
-// Every CTA of the cluster learns the totals of all CTAs: returns the sum of
-// the lower ranks' and, in `all`, of all.
-__device__ __forceinline__ int cluster_scan(int mine, int *slot, int &all) {
+// Every CTA of the cluster learns the totals of all CTAs: `tell`, a cluster barrier, `learn`, which
+// returns the sum of the lower ranks' and, in `all`, of all.
+__device__ __forceinline__ void tell(int mine, int *slot) {
   cg::cluster_group c = cg::this_cluster();
-  const int rank = c.block_rank();
-  if (threadIdx.x < kPlanCtas) *c.map_shared_rank(slot + rank, threadIdx.x) = mine;
-  c.sync();
+  if (threadIdx.x < kPlanCtas) *c.map_shared_rank(slot + c.block_rank(), threadIdx.x) = mine;
+}
+__device__ __forceinline__ int learn(const int *slot, int &all) {
+  const int rank = cg::this_cluster().block_rank();
   int before = 0;
   all = 0;
   for (int i = 0; i < kPlanCtas; ++i) {
@@ -86,53 +87,74 @@ struct Slice {
   int lo, hi;
 };
 __device__ __forceinline__ Slice slice_of(int total, int rank) {
-  const int per = ((total + kPlanCtas - 1) / kPlanCtas + 3) & ~3;
+  const int per = ((total + kPlanCtas - 1) / kPlanCtas + 31) & ~31;
   const int lo = min(total, rank * per);
   return {lo, min(total, lo + per)};
 }
 
-// The page a thread scans in one turn of a slice: 4 in a row, -1 past the end.
-__device__ __forceinline__ int4 refs_at(const PoolArgs &a, int p, int hi) {
-  int4 r = make_int4(-1, -1, -1, -1);
-  if (p + 3 < hi) return *reinterpret_cast<const int4 *>(a.refs + p);
-  if (p < hi) r.x = a.refs[p];
-  if (p + 1 < hi) r.y = a.refs[p + 1];
-  if (p + 2 < hi) r.z = a.refs[p + 2];
-  return r;
+// A slice in words of 32 pages: a warp takes `words` words in a row, at most 32, and lane j keeps
+// word j as bits, so that ranks are exclusive sums over threads and a word's pages are read and
+// listed side by side.  A CTA's round is at most 32 K pages: the pools of a GPU's memory take one or a few.
+struct Words {
+  int words, round;  // of a warp; pages of the CTA
+  __device__ explicit Words(const Slice &s)
+      : words(min(32, max(1, (s.hi - s.lo + 1023) / 1024))), round(words * 1024) {}
+  __device__ int first(int p0) const { return p0 + (threadIdx.x >> 5) * words * 32; }  // of the warp
+};
+// The warp's words from page p on: pages in use, or free ones.
+template <bool kFree>
+__device__ __forceinline__ uint32_t page_bits(const PoolArgs &a, int p, int hi, int words) {
+  const int lane = threadIdx.x & 31;
+  uint32_t mine = 0;
+  for (int w0 = 0; w0 < words; w0 += 8) {
+    int v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int q = p + 32 * (w0 + u) + lane;
+      v[u] = w0 + u < words && q < hi ? a.refs[q] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t bits = __ballot_sync(0xffffffffu, kFree ? v[u] == 0 : v[u] > 0);
+      if (lane == w0 + u) mine = bits;
+    }
+  }
+  return mine;
 }
 
-// The free pages of rank 0 .. need-1 into list[rank].  Returns how many are free
-// (at least `need`, or all there are).
-__device__ int find_free(const PoolArgs &a, int need, int *list, int *warp_sums, int *slot) {
-  const int rank = cg::this_cluster().block_rank();
-  const Slice s = slice_of(a.pages, rank);
+// The free pages of the slice: their number (the thread's of the first round in `bits`).
+__device__ int count_free(const PoolArgs &a, const Slice &s, const Words &w, uint32_t &bits) {
   int count = 0;
-  for (int p = s.lo + 4 * threadIdx.x; p < s.hi; p += 4 * kPlanThreads) {
-    const int4 r = refs_at(a, p, s.hi);
-    count += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
+  for (int p0 = s.lo; p0 < s.hi; p0 += w.round) {
+    const uint32_t b = page_bits<true>(a, w.first(p0), s.hi, w.words);
+    if (p0 == s.lo) bits = b;
+    count += __popc(b);
   }
-  int total, all;
-  block_scan(count, warp_sums, total);
-  int base = cluster_scan(total, slot, all);
-  for (int p0 = s.lo; p0 < s.hi && base < need; p0 += 4 * kPlanThreads) {
-    const int p = p0 + 4 * threadIdx.x;
-    const int4 r = refs_at(a, p, s.hi);
-    const int f = (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
-    int k = base + block_scan(f, warp_sums, total);
-    const int v[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (v[i] == 0) {
-        if (k < need) list[k] = p + i;
-        ++k;
-      }
+  return count;
+}
+// The slice's free pages into list[base ...], as far as list[need - 1].
+__device__ void list_free(const PoolArgs &a, const Slice &s, const Words &w, uint32_t bits, int base, int need,
+                          int *list, int *warp_sums) {
+  const int lane = threadIdx.x & 31;
+  for (int p0 = s.lo; p0 < s.hi && base < need; p0 += w.round) {
+    const int p = w.first(p0);
+    if (p0 != s.lo) bits = page_bits<true>(a, p, s.hi, w.words);
+    int total;
+    const int k = base + block_scan(__popc(bits), warp_sums, total);
+    for (int j = 0; j < w.words; ++j) {
+      const uint32_t b = __shfl_sync(0xffffffffu, bits, j);
+      const int at = __shfl_sync(0xffffffffu, k, j) + __popc(b & ((1u << lane) - 1));
+      if ((b >> lane & 1) && at < need) list[at] = p + 32 * j + lane;
+    }
     base += total;
   }
-  return all;
 }
 
 // ---------------------------------------------------------------------------
-// Grow and fork.  Demands of the list's entries -> ranks -> free pages -> tables.
+// Grow and fork.  Demands of the list's entries -> ranks -> free pages -> tables.  Bound by the
+// latency of about eight dependent reads of L2 and three cluster barriers: a fork of 32 in a pool of 4096 pages takes
+// 12 us with its copy; 40 requests freed and 40 grown by up to 1024 blocks in 200,003 pages 21 us
+// (33 with 32 pages to a thread in place of a word of 32 to a warp, 43 with four).
 // ---------------------------------------------------------------------------
 struct ForkNeed {
   bool ok;
@@ -157,10 +179,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
   pdl_launch();
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), lane = threadIdx.x & 31;
-  const int gwarp = (rank * kPlanThreads + threadIdx.x) >> 5;
+  const int gwarp = (threadIdx.x >> 5) * kPlanCtas + rank;  // a short list goes over all CTAs
   constexpr int kGWarps = kPlanCtas * kPlanWarps;
   int32_t *from = a.work + kWorkHead, *to = from + a.span, *third = to + a.span;
 
+  cluster.barrier_arrive();  // (every CTA runs before another writes its shared memory)
+  const Slice slice = slice_of(a.pages, rank);
+  const Words words(slice);
+  uint32_t bits = 0;
+  int total;
+  block_scan(count_free(a, slice, words, bits), warp_sums, total);
   // demand of each entry; INT_MIN marks one that is skipped
   for (int i = gwarp; i < a.n; i += kGWarps) {
     int need = INT_MIN;
@@ -169,6 +197,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
       bool empty = f.ok;
       if (f.ok) {
         const int32_t *row = a.tables + static_cast<int64_t>(a.dst[i]) * a.blocks;
+#pragma unroll 8
         for (int b = lane; b < a.blocks; b += 32) empty &= row[b] == -1;
       }
       if (__all_sync(0xffffffffu, empty)) need = f.last >= 0 ? 1 : 0;
@@ -177,6 +206,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
       if (r >= 0 && r < a.R && w >= 0 && w <= a.blocks) {
         const int32_t *row = a.tables + static_cast<int64_t>(r) * a.blocks;
         int k = 0;
+#pragma unroll 8
         for (int b = lane; b < w; b += 32) k += row[b] == -1;
         need = __reduce_add_sync(0xffffffffu, k);
       }
@@ -186,6 +216,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
       if (need == INT_MIN) report(a, HISPARSE_ERR_RANGE);
     }
   }
+  cluster.barrier_wait();
+  tell(total, slot);
   cluster.sync();
   // every CTA ranks the whole list: thread t takes a run of entries
   const int run = (a.n + kPlanThreads - 1) / kPlanThreads;
@@ -194,7 +226,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
   for (int i = i0; i < i1; ++i) mine += max(0, third[i]);
   int demand;
   int at = block_scan(mine, warp_sums, demand);
-  const int free_pages = find_free(a, min(demand, a.pages), to, warp_sums, slot);
+  int free_pages;
+  const int before = learn(slot, free_pages);
+  list_free(a, slice, words, bits, before, min(demand, a.pages), to, warp_sums);
   // the demands that fit are a prefix of the list; `from` keeps each entry's first rank
   for (int i = i0; i < i1; ++i) {
     const int need = max(0, third[i]);
@@ -249,16 +283,29 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
         continue;
       }
       int32_t *row = a.tables + static_cast<int64_t>(a.src[i]) * a.blocks;
-      for (int b0 = 0; b0 < a.want[i]; b0 += 32) {
-        const int b = b0 + lane;
-        const bool hole = b < a.want[i] && row[b] == -1;
-        const unsigned m = __ballot_sync(0xffffffffu, hole);
-        if (hole) {
-          const int p = to[r + __popc(m & ((1u << lane) - 1))];
-          row[b] = p;
-          a.refs[p] = 1;
+      const int w = a.want[i];
+      for (int b0 = 0; b0 < w; b0 += 8 * 32) {
+        bool hole[8];
+        int at[8], page[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int b = b0 + 32 * u + lane;
+          hole[u] = b < w && row[b] == -1;
         }
-        r += __popc(m);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const unsigned m = __ballot_sync(0xffffffffu, hole[u]);
+          at[u] = r + __popc(m & ((1u << lane) - 1));
+          r += __popc(m);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) page[u] = hole[u] ? to[at[u]] : 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (hole[u]) {
+            row[b0 + 32 * u + lane] = page[u];
+            a.refs[page[u]] = 1;
+          }
       }
     }
   }
@@ -276,39 +323,48 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PoolAr
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank();
   int32_t *from = a.work + kWorkHead, *to = from + a.span, *moved = to + a.span;
+  const int lane = threadIdx.x & 31;
   const Slice s = slice_of(a.pages, rank);
-  int count = 0, total, m, low;
-  cluster.sync();  // every CTA of the cluster runs: its shared memory may be written
-  for (int p = s.lo + 4 * threadIdx.x; p < s.hi; p += 4 * kPlanThreads) {
-    const int4 r = refs_at(a, p, s.hi);
-    count += (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
+  const Words words(s);
+  int total, m, low;
+  cluster.barrier_arrive();  // (every CTA runs before another writes its shared memory)
+  uint32_t bits = 0;
+  int count = 0;
+  for (int p0 = s.lo; p0 < s.hi; p0 += words.round) {
+    const uint32_t b = page_bits<false>(a, words.first(p0), s.hi, words.words);
+    if (p0 == s.lo) bits = b;
+    count += __popc(b);
   }
   block_scan(count, warp_sums, total);
-  const int before = cluster_scan(total, slot, m);
+  cluster.barrier_wait();
+  tell(total, slot);
+  cluster.sync();
+  const int before = learn(slot, m);
   // used pages below m
   count = 0;
-  for (int p = s.lo + 4 * threadIdx.x; p < min(s.hi, m); p += 4 * kPlanThreads) {
-    const int4 r = refs_at(a, p, s.hi);
-    const int v[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) count += v[i] > 0 && p + i < m;
+  for (int p0 = s.lo; p0 < min(s.hi, m); p0 += words.round) {
+    const int p = words.first(p0), below = m - (p + 32 * lane);  // of this lane's word
+    const uint32_t b = p0 == s.lo ? bits : page_bits<false>(a, p, s.hi, words.words);
+    count += __popc(b & (below >= 32 ? ~0u : below > 0 ? (1u << below) - 1 : 0u));
   }
   block_scan(count, warp_sums, total);
-  cluster_scan(total, slot2, low);
+  tell(total, slot2);
+  cluster.sync();
+  learn(slot2, low);
   int base = before;
-  for (int p0 = s.lo; p0 < s.hi; p0 += 4 * kPlanThreads) {
-    const int p = p0 + 4 * threadIdx.x;
-    const int4 r = refs_at(a, p, s.hi);
-    const int v[4] = {r.x, r.y, r.z, r.w};
-    int used = base + block_scan((r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0), warp_sums, total);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (p + i >= s.hi) break;
-      if (v[i] > 0) {
-        if (p + i >= m) from[used - low] = p + i;
-        ++used;
-      } else if (p + i < m) {
-        to[p + i - used] = p + i;
+  for (int p0 = s.lo; p0 < s.hi; p0 += words.round) {
+    const int p = words.first(p0);
+    if (p0 != s.lo) bits = page_bits<false>(a, p, s.hi, words.words);
+    const int k = base + block_scan(__popc(bits), warp_sums, total);
+    for (int j = 0; j < words.words; ++j) {
+      const uint32_t b = __shfl_sync(0xffffffffu, bits, j);
+      const int used = __shfl_sync(0xffffffffu, k, j) + __popc(b & ((1u << lane) - 1));
+      const int q = p + 32 * j + lane;
+      if (q >= s.hi) continue;
+      if (b >> lane & 1) {
+        if (q >= m) from[used - low] = q;
+      } else if (q < m) {
+        to[q - used] = q;
       }
     }
     base += total;
@@ -329,12 +385,16 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PoolAr
 
 // ---------------------------------------------------------------------------
 // page_copy_kernel: the bytes of the plan's pages in every layer, in 16-byte
-// chunks over the whole grid, kUnroll reads of a thread in flight.  For a
+// chunks over the whole grid, kCopyUnroll reads of a thread in flight.  For a
 // fork, copy i goes to the part-filled block of its destination's table row.  For a
-// compaction the table entries above the used pages follow their pages too.
+// compaction the table entries above the used pages follow their pages too.  Bound by one
+// read and one write of the pages: 1.7 thousand pages of 36 KB in 4 layers (512 MB of traffic) take 88 us with
+// their plan, 5.8 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 512;
-constexpr int kCopyUnroll = 8;
+constexpr int kCopyUnroll = 4;
+constexpr int kCopyCtas = 152 * 4;
+constexpr int kPiece = 1024;  // 16-byte chunks
 
 template <bool kFork>
 __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const PoolArgs a) {
@@ -357,32 +417,40 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const PoolArgs 
       }
     }
   }
-  // one CTA to a (copy, layer) pair in turn
-  const int64_t items = static_cast<int64_t>(copies) * a.layers;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int c = static_cast<int>(it / a.layers), l = static_cast<int>(it - static_cast<int64_t>(c) * a.layers);
-    int rows = a.page_tokens, dst;
+  // Pieces of 16 KB (or a page, where it is smaller) of every copy in every layer, a half CTA to a
+  // piece in turn; pages under 1 KB a warp to a page.
+  const int64_t page = static_cast<int64_t>(a.page_tokens) * a.row_bytes / 16;  // chunks of 16 bytes
+  const int pieces = static_cast<int>((page + kPiece - 1) / kPiece);
+  const int team = page <= 64 ? 32 : 256;  // threads to a piece
+  const int64_t items = static_cast<int64_t>(copies) * a.layers * pieces;
+  const int in = threadIdx.x & (team - 1);
+  for (int64_t it = tid / team; it < items; it += step / team) {
+    const int64_t cl = it / pieces;
+    const int64_t first = (it - cl * pieces) * kPiece;
+    const int c = static_cast<int>(cl / a.layers), l = static_cast<int>(cl - static_cast<int64_t>(c) * a.layers);
+    int64_t chunks = page;
+    int dst;
     if (kFork) {
-      rows = third[c];
-      if (rows == 0) continue;
+      chunks = third[c] * a.row_bytes / 16;
+      if (chunks <= first) continue;
       dst = a.tables[static_cast<int64_t>(a.dst[c]) * a.blocks + a.want[c] / a.page_tokens];
       if (dst < 0 || dst >= a.pages) continue;
     } else {
       dst = to[c];
     }
     const uint4 *s = reinterpret_cast<const uint4 *>(a.store + l * a.layer_stride +
-                                                     static_cast<int64_t>(from[c]) * a.page_stride);
+                                                     static_cast<int64_t>(from[c]) * a.page_stride) + first;
     uint4 *d = reinterpret_cast<uint4 *>(a.store + l * a.layer_stride +
-                                         static_cast<int64_t>(dst) * a.page_stride);
-    const int64_t chunks = rows * a.row_bytes / 16;
-    for (int64_t i = threadIdx.x; i < chunks; i += kCopyThreads * kCopyUnroll) {
+                                         static_cast<int64_t>(dst) * a.page_stride) + first;
+    const int n = static_cast<int>(min(static_cast<int64_t>(kPiece), chunks - first));
+    for (int i = in; i < n; i += team * kCopyUnroll) {
       uint4 v[kCopyUnroll];
 #pragma unroll
       for (int u = 0; u < kCopyUnroll; ++u)
-        if (i + u * kCopyThreads < chunks) v[u] = s[i + u * kCopyThreads];
+        if (i + u * team < n) v[u] = __ldcs(s + i + u * team);
 #pragma unroll
       for (int u = 0; u < kCopyUnroll; ++u)
-        if (i + u * kCopyThreads < chunks) d[i + u * kCopyThreads] = v[u];
+        if (i + u * team < n) __stcs(d + i + u * team, v[u]);
     }
   }
 }
@@ -459,9 +527,10 @@ int hisparse_pages_fork(const hisparse_page_pool *p, const int32_t *d_src, const
   if (const int rc = launch_pdl(plan_kernel<true>, dim3(kPlanCtas), dim3(kPlanThreads), 0, stream,
                                 kPlanCtas, a))
     return rc;
-  const int64_t items = static_cast<int64_t>(n) * a.layers;
-  return launch_pdl(page_copy_kernel<true>, dim3(static_cast<unsigned>(std::min<int64_t>(items, 456))),
-                    dim3(kCopyThreads), 0, stream, 1, a);
+  const int64_t page = static_cast<int64_t>(a.page_tokens) * a.row_bytes / 16;
+  const int64_t threads = static_cast<int64_t>(n) * a.layers * ((page + kPiece - 1) / kPiece) * (page <= 64 ? 32 : 256);
+  const int64_t ctas = std::min<int64_t>(kCopyCtas, (threads + kCopyThreads - 1) / kCopyThreads);
+  return launch_pdl(page_copy_kernel<true>, dim3(static_cast<unsigned>(ctas)), dim3(kCopyThreads), 0, stream, 1, a);
 }
 
 int hisparse_pages_free(const hisparse_page_pool *p, const int32_t *d_reqs, int32_t n,
@@ -481,7 +550,7 @@ int hisparse_pages_compact(const hisparse_page_pool *p, void *stream) {
   if (const int rc = launch_pdl(compact_plan_kernel, dim3(kPlanCtas), dim3(kPlanThreads), 0, stream,
                                 kPlanCtas, a))
     return rc;
-  return launch_pdl(page_copy_kernel<false>, dim3(304), dim3(kCopyThreads), 0, stream, 1, a);
+  return launch_pdl(page_copy_kernel<false>, dim3(kCopyCtas), dim3(kCopyThreads), 0, stream, 1, a);
 }
 
 }  // extern "C"
