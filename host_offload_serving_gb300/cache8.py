@@ -40,7 +40,7 @@ def _need(ok, message):
 
 def _i32(t, what, numel=None):
     if t is None:
-        return None
+        return 0
     if t.dtype is not torch.int32 or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous int32 tensor expected")
     if numel is not None and t.numel() != numel:
@@ -59,8 +59,7 @@ class Records:
         self.block_tokens, self.latent = int(block_tokens), bool(latent)
         self.columns = self.kv_heads * (1 if latent else 2)
         self.row_bytes = self.kv_heads * (self.k_dim + (0 if latent else self.v_dim))
-        self.c = H.Records(self.kv_heads, self.k_dim, self.v_dim, int(self.latent),
-                           self.block_tokens)
+        self.c = (self.kv_heads, self.k_dim, self.v_dim, int(self.latent), self.block_tokens)
 
     def blocks(self, positions):
         """Scale blocks that ``positions`` positions need."""
@@ -101,16 +100,19 @@ def rotary_turns(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len
                         dtype=torch.int64), amplitude
 
 
-def _rotary_tensor(t, x, y, tokens, what):
-    if x.dim() != 3 or x.shape[0] != tokens or x.shape != y.shape or x.dtype is not y.dtype:
+def _rotary_tensor(x, y, tokens, what):
+    """The fields of one rotated tensor."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != tokens or (y is not x and (shape != y.shape or x.dtype is not y.dtype)):
         raise ValueError(f"rotate: {what} and its output are [tokens][heads][dim] of one type")
-    xs, ys = x.stride(), y.stride()
+    xs = x.stride()
+    ys = xs if y is x else y.stride()
     if xs[2] != 1 or ys[2] != 1:
         raise ValueError(f"rotate: the values of a head of {what} are contiguous")
-    t.x, t.y = x.data_ptr(), y.data_ptr()
-    t.x_token_stride, t.x_head_stride = xs[0], xs[1]
-    t.y_token_stride, t.y_head_stride = ys[0], ys[1]
-    t.heads, t.dim = x.shape[1], x.shape[2]
+    return x.data_ptr(), y.data_ptr(), xs[0], xs[1], ys[0], ys[1], shape[1], shape[2]
+
+
+_NO_TENSOR = (0,) * 8
 
 
 def rotate(x, positions, turns, *, k=None, out=None, k_out=None, offset=0, interleaved=False,
@@ -120,20 +122,19 @@ def rotate(x, positions, turns, *, k=None, out=None, k_out=None, offset=0, inter
     ``out`` in place.  ``positions`` int32 [tokens]; ``turns`` int64 on the
     device.  ``inverse`` turns back (the gradient of a rotation).  Strided views are taken as they
     are.  Returns (out, k_out)."""
-    a = H.RotaryArgs()
     out = x if out is None else out
-    a.dtype = _dtype(x, "rotate")
-    a.tokens = x.shape[0]
-    _rotary_tensor(a.t[0], x, out, a.tokens, "x")
+    dtype = _dtype(x, "rotate")
+    tokens = x.shape[0]
+    first, second = _rotary_tensor(x, out, tokens, "x"), _NO_TENSOR
     if k is not None:
         k_out = k if k_out is None else k_out
         _need(k.dtype is x.dtype, "rotate: x and k are of one type")
-        _rotary_tensor(a.t[1], k, k_out, a.tokens, "k")
+        second = _rotary_tensor(k, k_out, tokens, "k")
     if turns.dtype is not torch.int64 or not turns.is_contiguous():
         raise ValueError("rotate: turns is a contiguous int64 tensor")
-    a.rot_dim, a.offset, a.amplitude = 2 * turns.numel(), offset, amplitude
-    a.flags = (H.ROTARY_INTERLEAVED if interleaved else 0) | (H.ROTARY_INVERSE if inverse else 0)
-    a.d_positions, a.d_turns = _i32(positions, "rotate: positions", a.tokens), turns.data_ptr()
+    flags = (H.ROTARY_INTERLEAVED if interleaved else 0) | (H.ROTARY_INVERSE if inverse else 0)
+    a = H.pack_rotary(dtype, 2 * turns.numel(), offset, flags, tokens, amplitude,
+                      _i32(positions, "rotate: positions", tokens), turns.data_ptr(), *first, *second)
     H.check(H.hisparse_rotary(a, _stream(stream)), "hisparse_rotary")
     return out, k_out
 
@@ -150,50 +151,47 @@ def pack(rec, k, v, dst, scales, start, *, cu_lens=None, reqs=None, max_len=1, h
     [R][P][row_bytes], by position; or, with the page table ``blocks`` int32
     [R][max_blocks], a store [rows][row_bytes] of pages of ``page_tokens`` rows.  ``turns``:
     K is rotated on the way.  See hisparse_pack for the scales."""
-    a = H.PackArgs()
-    a.rec = rec.c
-    a.dtype = _dtype(k, "pack")
-    a.tokens = k.shape[0]
-    ks = k.stride()
-    if k.dim() != 3 or k.shape[1] != rec.kv_heads or k.shape[2] != rec.k_dim or ks[2] != 1:
+    dtype = _dtype(k, "pack")
+    shape, ks = k.shape, k.stride()
+    if len(shape) != 3 or shape[1] != rec.kv_heads or shape[2] != rec.k_dim or ks[2] != 1:
         raise ValueError("pack: k is [tokens][kv_heads][k_dim]")
-    a.k, a.k_token_stride, a.k_head_stride = k.data_ptr(), ks[0], ks[1]
+    tokens = shape[0]
+    v_ptr, vs = 0, (0, 0)
     if not rec.latent:
-        if v is None or v.shape != (a.tokens, rec.kv_heads, rec.v_dim) or v.dtype is not k.dtype \
+        if v is None or v.shape != (tokens, rec.kv_heads, rec.v_dim) or v.dtype is not k.dtype \
                 or v.stride(2) != 1:
             raise ValueError("pack: v is [tokens][kv_heads][v_dim] of k's type")
-        a.v, a.v_token_stride, a.v_head_stride = v.data_ptr(), v.stride(0), v.stride(1)
+        v_ptr, vs = v.data_ptr(), v.stride()
     elif v is not None:
         raise ValueError("pack: a latent record has no v")
-    if scales.dtype is not torch.float32 or scales.dim() != 3 or scales.shape[2] != rec.columns \
-            or scales.stride(2) != 1 or scales.stride(1) != rec.columns:
+    cs, ss = scales.shape, scales.stride()
+    if scales.dtype is not torch.float32 or len(cs) != 3 or cs[2] != rec.columns or ss[2] != 1 \
+            or ss[1] != rec.columns:
         raise ValueError("pack: scales are float32 [R][blocks][columns]")
-    a.n, a.max_len, a.headroom = start.numel(), max_len, headroom
-    a.num_requests, a.scale_blocks = scales.shape[0], scales.shape[1]
-    a.scales, a.scales_req_stride = scales.data_ptr(), scales.stride(0)
-    a.d_start = _i32(start, "pack: start")
-    a.d_cu_lens = _i32(cu_lens, "pack: cu_lens", a.n + 1)
-    a.d_reqs = _i32(reqs, "pack: reqs", a.n)
-    if reqs is None:
-        _need(a.n <= a.num_requests, "pack: more sequences than requests")
-    ds = dst.stride()
-    if dst.dtype is not torch.uint8 or dst.shape[-1] != rec.row_bytes or ds[-1] != 1:
+    n, R = start.numel(), cs[0]
+    _need(reqs is not None or n <= R, "pack: more sequences than requests")
+    rows, ds = dst.shape, dst.stride()
+    if dst.dtype is not torch.uint8 or rows[-1] != rec.row_bytes or ds[-1] != 1:
         raise ValueError("pack: dst is uint8 [..][row_bytes]")
-    a.dst, a.dst_rows, a.dst_row_stride = dst.data_ptr(), dst.shape[-2], ds[-2]
-    if dst.dim() == 3:
-        if dst.shape[0] != a.num_requests or blocks is not None:
+    req_stride = table = max_blocks = 0
+    if len(rows) == 3:
+        if rows[0] != R or blocks is not None:
             raise ValueError("pack: dst by position is [R][P][row_bytes], without a page table")
         # one request, or an expanded one, still goes by position
-        a.dst_req_stride = ds[0] if dst.shape[0] > 1 else max(16, ds[0])
+        req_stride = ds[0] if R > 1 else max(16, ds[0])
     if blocks is not None:
-        a.d_blocks = _i32(blocks, "pack: blocks")
-        _need(blocks.shape[0] == a.num_requests, "pack: blocks is [R][max_blocks]")
-        a.max_blocks, a.page_tokens = blocks.shape[1], page_tokens
+        table, max_blocks = _i32(blocks, "pack: blocks"), blocks.shape[1]
+        _need(blocks.shape[0] == R, "pack: blocks is [R][max_blocks]")
+    else:
+        page_tokens = 0
+    rot = (0, 0, 0, 0.0, 0)
     if turns is not None:
-        a.rot_dim, a.rot_offset, a.amplitude = 2 * turns.numel(), rot_offset, amplitude
-        a.rot_flags = H.ROTARY_INTERLEAVED if interleaved else 0
-        a.d_turns = turns.data_ptr()
-    a.d_status = _i32(status, "pack: status")
+        rot = (2 * turns.numel(), rot_offset, H.ROTARY_INTERLEAVED if interleaved else 0, amplitude,
+               turns.data_ptr())
+    a = H.pack_pack(*rec.c, dtype, n, max_len, R, cs[1], headroom, _i32(cu_lens, "pack: cu_lens", n + 1),
+                    _i32(start, "pack: start"), _i32(reqs, "pack: reqs", n), tokens, k.data_ptr(), v_ptr,
+                    ks[0], ks[1], vs[0], vs[1], scales.data_ptr(), ss[0], dst.data_ptr(), rows[-2], ds[-2],
+                    req_stride, table, max_blocks, page_tokens, *rot, _i32(status, "pack: status"))
     H.check(H.hisparse_pack(a, _stream(stream)), "hisparse_pack")
     return dst
 
@@ -206,50 +204,42 @@ def attend(rec, q, sel, slots, hot, scales, out, *, softmax_scale=None, lse=None
     [R][B + 1][record_tokens * row_bytes] and ``resident`` [rows][same], into
     ``out`` [R][rows][heads][v_dim]; ``lse`` float32 [R][rows][heads] optional.
     ``scales`` [R][blocks][columns].  See hisparse_attend."""
-    a = H.AttendArgs()
-    a.rec = rec.c
-    a.dtype = _dtype(q, "attend")
-    if q.dim() != 4 or q.shape[3] != rec.k_dim or out.dim() != 4 or out.shape[:3] != q.shape[:3] \
-            or out.shape[3] != rec.v_dim or out.dtype is not q.dtype:
+    dtype = _dtype(q, "attend")
+    shape, to = q.shape, out.shape
+    if len(shape) != 4 or shape[3] != rec.k_dim or len(to) != 4 or to[:3] != shape[:3] \
+            or to[3] != rec.v_dim or out.dtype is not q.dtype:
         raise ValueError("attend: q is [R][rows][heads][k_dim], out [R][rows][heads][v_dim], of one type")
-    R, rows, heads, _ = q.shape
+    R, rows, heads, _ = shape
     qs, os = q.stride(), out.stride()
     if qs[3] != 1 or os[3] != 1 or (rows > 1 and R > 1 and (qs[0] != rows * qs[1] or os[0] != rows * os[1])):
         raise ValueError("attend: q and out have one stride from row to row, and contiguous heads")
-    a.num_requests, a.rows, a.heads = R, rows, heads
     by = 0 if rows == 1 else 1
-    a.q, a.q_row_stride, a.q_head_stride = q.data_ptr(), qs[by], qs[2]
-    a.out, a.out_row_stride, a.out_head_stride = out.data_ptr(), os[by], os[2]
-    if slots.dim() != 2 or slots.shape[0] != R or slots.shape[1] % rows:
+    listed = slots.shape
+    if len(listed) != 2 or listed[0] != R or listed[1] % rows:
         raise ValueError("attend: slots is [R][rows * entries]")
-    a.entries = slots.shape[1] // rows
-    a.sel_block_tokens = sel_block_tokens
-    a.d_slots = _i32(slots, "attend: slots")
-    a.d_sel = _i32(sel, "attend: sel", slots.numel() // max(1, sel_block_tokens))
-    hs = hot.stride()
-    if hot.dtype is not torch.uint8 or hot.dim() != 3 or hot.shape[0] != R or hs[2] != 1 \
-            or hot.shape[2] != record_tokens * rec.row_bytes:
+    d_slots = _i32(slots, "attend: slots")
+    d_sel = _i32(sel, "attend: sel", R * listed[1] // max(1, sel_block_tokens))
+    hot_shape, hs = hot.shape, hot.stride()
+    if hot.dtype is not torch.uint8 or len(hot_shape) != 3 or hot_shape[0] != R or hs[2] != 1 \
+            or hot_shape[2] != record_tokens * rec.row_bytes:
         raise ValueError("attend: hot is uint8 [R][B + 1][record_tokens * row_bytes]")
-    a.buffer_slots, a.record_tokens = hot.shape[1] - 1, record_tokens
-    a.hot, a.hot_req_stride, a.hot_row_stride = hot.data_ptr(), hs[0], hs[1]
+    store = (0, 0, 0)
     if resident is not None:
         if resident.dtype is not torch.uint8 or resident.dim() != 2 or resident.stride(1) != 1 \
-                or resident.shape[1] != hot.shape[2]:
+                or resident.shape[1] != hot_shape[2]:
             raise ValueError("attend: resident is uint8 [rows][record_tokens * row_bytes]")
-        a.resident, a.resident_rows = resident.data_ptr(), resident.shape[0]
-        a.resident_row_stride = resident.stride(0)
-    if scales.dtype is not torch.float32 or scales.dim() != 3 or scales.shape[0] != R \
-            or scales.shape[2] != rec.columns or scales.stride(2) != 1 \
-            or scales.stride(1) != rec.columns:
+        store = (resident.data_ptr(), resident.shape[0], resident.stride(0))
+    cs, ss = scales.shape, scales.stride()
+    if scales.dtype is not torch.float32 or len(cs) != 3 or cs[0] != R or cs[2] != rec.columns \
+            or ss[2] != 1 or ss[1] != rec.columns:
         raise ValueError("attend: scales are float32 [R][blocks][columns]")
-    a.scales, a.scales_req_stride, a.scale_blocks = scales.data_ptr(), scales.stride(0), scales.shape[1]
-    if lse is not None:
-        if lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.shape != q.shape[:3]:
-            raise ValueError("attend: lse is float32 [R][rows][heads]")
-        a.lse = lse.data_ptr()
-    a.softmax_scale = rec.k_dim ** -0.5 if softmax_scale is None else softmax_scale
-    a.d_seq_lens = _i32(seq_lens, "attend: seq_lens", R)
-    a.d_num_reqs = _i32(num_reqs, "attend: num_reqs", 1)
-    a.d_status = _i32(status, "attend: status")
+    if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.shape != shape[:3]):
+        raise ValueError("attend: lse is float32 [R][rows][heads]")
+    a = H.pack_attend(*rec.c, dtype, R, rows, listed[1] // rows, heads, hot_shape[1] - 1, record_tokens,
+                      sel_block_tokens, rec.k_dim ** -0.5 if softmax_scale is None else softmax_scale,
+                      q.data_ptr(), qs[by], qs[2], out.data_ptr(), os[by], os[2],
+                      0 if lse is None else lse.data_ptr(), d_sel, d_slots, hot.data_ptr(), hs[0], hs[1],
+                      *store, scales.data_ptr(), ss[0], cs[1], _i32(seq_lens, "attend: seq_lens", R),
+                      _i32(num_reqs, "attend: num_reqs", 1), _i32(status, "attend: status"))
     H.check(H.hisparse_attend(a, _stream(stream)), "hisparse_attend")
     return out

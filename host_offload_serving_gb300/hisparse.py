@@ -7,6 +7,7 @@ library cannot be built or loaded the import fails -- there is no fallback.
 """
 import ctypes
 import os
+import struct
 
 from . import _build
 
@@ -90,6 +91,24 @@ class PagePool(ctypes.Structure):
                 ("d_refs", _vp), ("d_work", _vp), ("d_status", _vp)]
 
 
+def packer(cls):
+    """The values of a structure, in the order of its fields and theirs, into its bytes: a quarter of
+    the time that setting them one by one takes."""
+    codes = {_i32: "i", _u32: "I", _i64: "q", _f32: "f", _vp: "P"}
+
+    def code(t):
+        if issubclass(t, ctypes.Array):
+            return code(t._type_) * t._length_
+        if issubclass(t, ctypes.Structure):
+            return "".join(code(f) for _, f in t._fields_)
+        return codes[t]
+    s = struct.Struct(code(cls) + "0q")
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+pack_rotary, pack_pack, pack_attend = packer(RotaryArgs), packer(PackArgs), packer(AttendArgs)
+
 # (name, restype, argtypes) of every exported symbol, in header order
 SIGNATURES = [
     ("hisparse_init", _i32, [ctypes.POINTER(Config), ctypes.POINTER(LayerBuffers),
@@ -111,9 +130,9 @@ SIGNATURES = [
     ("hisparse_export_plan", _i32, [_vp, _i32, _vp, _vp, _vp]),
     ("hisparse_reset", _i32, [_vp, _i32, _vp]),
     ("hisparse_set_l2_persisting", _i32, [_vp, _i64]),
-    ("hisparse_rotary", _i32, [ctypes.POINTER(RotaryArgs), _vp]),
-    ("hisparse_pack", _i32, [ctypes.POINTER(PackArgs), _vp]),
-    ("hisparse_attend", _i32, [ctypes.POINTER(AttendArgs), _vp]),
+    ("hisparse_rotary", _i32, [_vp, _vp]),
+    ("hisparse_pack", _i32, [_vp, _vp]),
+    ("hisparse_attend", _i32, [_vp, _vp]),
     ("hisparse_pages_work_ints", _i64, [_i32, _i32]),
     ("hisparse_pages_grow", _i32, [ctypes.POINTER(PagePool), _vp, _vp, _i32, _vp]),
     ("hisparse_pages_fork", _i32, [ctypes.POINTER(PagePool), _vp, _vp, _vp, _i32, _vp]),
@@ -284,16 +303,17 @@ def hisparse_admit(h, layer, d_reqs, n, d_preload, stream):
 
 
 # ---- 8-bit records and resident pages --------------------------------------
+# (args: the structure, or its bytes)
 def hisparse_rotary(args, stream):
-    return load().hisparse_rotary(args, stream)
+    return load().hisparse_rotary(args if type(args) is bytes else ctypes.byref(args), stream)
 
 
 def hisparse_pack(args, stream):
-    return load().hisparse_pack(args, stream)
+    return load().hisparse_pack(args if type(args) is bytes else ctypes.byref(args), stream)
 
 
 def hisparse_attend(args, stream):
-    return load().hisparse_attend(args, stream)
+    return load().hisparse_attend(args if type(args) is bytes else ctypes.byref(args), stream)
 
 
 def hisparse_pages_work_ints(num_pages, num_requests):
