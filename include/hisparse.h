@@ -575,13 +575,16 @@ typedef struct {
  *   amax / 448 over the call's tokens of the block, times `headroom` unless the
  *   call also holds the block's last position (amax 0 leaves it 0, not set);
  * - else the block is open and its scale stands.
- * A value x is stored as e4m3(x / scale), rounded to nearest even, saturating
- * at 448; infinities do not count in amax and saturate; NaN stays NaN.  A decode step's
+ * A value x is stored as e4m3(x * (1 / scale)), rounded to nearest even, saturating
+ * at 448; infinities do not count in amax and saturate; NaN stays NaN.  A scale is at least
+ * 2^-100.  A decode step's
  * rows are d_new_rows of hisparse_resolve_step; a prompt's go to the host pool,
  * a mirror or the resident store.  Start the scales of a new request at 0.
  * A position outside [0, scale_blocks * block_tokens), a request outside
- * [0, R), or a row outside dst sets HISPARSE_ERR_RANGE; its token is skipped.
- * Errors: EINVAL, EBOUND (sizes of hisparse_records), ECUDA. */
+ * [0, R), a sequence that passes position 2^31 - 1, or a row outside dst sets
+ * HISPARSE_ERR_RANGE; its tokens are skipped.  k, v and dst are 16-byte aligned, strides of
+ * k and v multiples of 8 elements.
+ * Errors: EINVAL, EBOUND (sizes of hisparse_records; more than 65535 sequences), ECUDA. */
 int hisparse_pack(const hisparse_pack_args *args, void *stream);
 
 typedef struct {
@@ -621,11 +624,16 @@ typedef struct {
  *   s_j = softmax_scale * q . (k_j * sK),  out = sum_j softmax(s)_j (v_j * sV),
  * lse = log sum_j exp(s_j).  A row with nothing to read gives out 0 and lse
  * -inf.  Scores, softmax and sums are in 32 bits; K and V enter the tensor
- * cores as the e4m3 they are, q and the probabilities as sums of e4m3 terms
- * (two for bf16, three for f16) at least as fine as their type.  A slot
+ * cores as the e4m3 they are, q and the probabilities as sums of 8-bit terms, two for
+ * bf16 and three for f16: q at least as fine as its type, a probability p within
+ * max(2^-8 p, 2^-16 of the row's largest) (f16: 2^-13, 2^-20).  A scale of V below 2^-100 counts as 2^-100.  A slot
  * outside what B, resident and -1 allow, or a selected position outside
- * the scale table, sets HISPARSE_ERR_RANGE and is left out.
- * Errors: EINVAL, EBOUND (sizes of hisparse_records), ECUDA. */
+ * the scale table or of 2^31 or more, sets HISPARSE_ERR_RANGE and is left out.
+ * HISPARSE_ERR_WAIT: a wait inside the kernel ran out (it ends; its outputs do not count).
+ * Results do not depend on timing.  q, out, hot and resident are 16-byte aligned.
+ * Errors: EINVAL; EBOUND (sizes of hisparse_records; more than 65535 heads, tokens of a record
+ * or of a selected block; 2^28 rows of q; 2^30 tokens of a row; 2^31 scales of a request; row strides of
+ * 4 GB); ECUDA. */
 int hisparse_attend(const hisparse_attend_args *args, void *stream);
 
 /* The pages of the resident tier: a store of num_pages pages of page_tokens
