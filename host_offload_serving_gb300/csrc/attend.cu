@@ -207,6 +207,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // OR over a group of four softmax warps, and their barrier (1 or 2: constants, as a CTA
 // takes all 16 hardware barriers for one that is not, and two such CTAs do not fit an SM).
 template <int kId>
@@ -613,12 +618,20 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     const int tk = wl * 32 + lane;
     const uint32_t p_row = base + a.off_p + tk * 128;
     bool seen = false;  // some token so far
-    for (int i = 0; i < tiles; ++i) {
-      const int cn = min(a.tile, t1 - t0 - i * a.tile);
+    constexpr bool kHeld = NC == 16;  // factors and offsets fit in registers
+    float qf[kHeld ? NC : 1], off[kHeld ? NC : 1];
+    if (kHeld) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) qf[kHeld ? c : 0] = s_qf[c0 + c], off[kHeld ? c : 0] = 0.f;
+    }
+    // This lane's token of a tile: its scale of K, and of V as log2 and inverse.
+    float ks, lv, iv;
+    bool use;
+    auto scales_of = [&](int i) {
       bar_wait(b_meta + 8 * (i % kTables), (i / kTables) & 1, fail);
-      float ks = 0.f, lv = 0.f, iv = 1.f;
-      bool use = false;
-      if (tk < cn) {
+      ks = 0.f, lv = 0.f, iv = 1.f;
+      use = false;
+      if (tk < min(a.tile, t1 - t0 - i * a.tile)) {
         float2 meta;
         asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
                      : "=f"(meta.x), "=f"(meta.y)
@@ -627,11 +640,15 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
         use = __float_as_int(meta.x) != 0x7fffffff;
         if (use) {
           ks = meta.x;
-          const float v = fmaxf(meta.y, 0x1p-100f);
-          lv = log2f(v);
-          iv = 1.f / v;
+          // (approximate to 2^-21, and the inverse of the very same)
+          lv = lg2(fmaxf(meta.y, 0x1p-100f));
+          iv = ex2(-lv);
         }
       }
+    };
+    if (tiles > 0) scales_of(0);
+    for (int i = 0; i < tiles; ++i) {
+      const int cn = min(a.tile, t1 - t0 - i * a.tile);
       bar_wait(b_s + 8 * (i & 1), (i >> 1) & 1, fail);
       __syncwarp();
       tc_after();
@@ -658,7 +675,13 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       float most = -INFINITY;
 #pragma unroll
       for (int c = 0; c < NC; c += 4) {
-        const float4 f = ld_shared4(smem_u32(s_qf + c0 + c)), m = ld_shared4(smem_u32(s_m + c0 + c));
+        float4 f, m;
+        if (kHeld) {
+          f = make_float4(qf[kHeld ? c : 0], qf[kHeld ? c + 1 : 0], qf[kHeld ? c + 2 : 0], qf[kHeld ? c + 3 : 0]);
+          m = make_float4(off[kHeld ? c : 0], off[kHeld ? c + 1 : 0], off[kHeld ? c + 2 : 0], off[kHeld ? c + 3 : 0]);
+        } else {
+          f = ld_shared4(smem_u32(s_qf + c0 + c)), m = ld_shared4(smem_u32(s_m + c0 + c));
+        }
         const float g[4] = {f.x, f.y, f.z, f.w}, o[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -713,7 +736,11 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
           for (int c = 0; c < NC; ++c) l[c] *= s_f[c0 + c];
         }
 #pragma unroll
-        for (int c = 0; c < NC; ++c) x[c] -= s_d[c0 + c];
+        for (int c = 0; c < NC; ++c) {
+          const float d = s_d[c0 + c];
+          x[c] -= d;
+          if (kHeld) off[kHeld ? c : 0] += d;
+        }
         seen = true;
       }
 #pragma unroll
@@ -721,6 +748,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
         x[c] = ex2(x[c]);
         l[c] = fmaf(x[c], iv, l[c]);
       }
+      if (i + 1 < tiles) scales_of(i + 1);  // while the products before are still under way
       if (!moved) previous();
       if (tk < ((cn + 31) & ~31)) {
 #pragma unroll
@@ -983,16 +1011,18 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       }
     } else {
       for (int i = 0; i < tiles; ++i) {
-        bar_wait(b_p, i & 1, fail);
-#pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-          // (a half without values may be gone and filled again by now: it is not waited for)
-          if (half_of(a, u).v0 < half_of(a, u).v1) bar_wait(b_full + 16 * s + 8 * u, turn & 1, fail);
+        // V's half is waited for, and made visible to the tensor cores, before the probabilities come.
+        // A latent record's halves were, by the warp that issued the scores that led to them.
+        if (!a.latent) {
+          bar_wait(b_full + 16 * s + 8, turn & 1, fail);
           fence_async();
           __syncwarp();
-          tc_after();
-          values(i, u);
         }
+        bar_wait(b_p, i & 1, fail);
+        __syncwarp();
+        tc_after();
+#pragma unroll 1
+        for (int u = a.latent ? 0 : 1; u < 2; ++u) values(i, u);
         if (++s == a.stages) s = 0, ++turn;
       }
     }
