@@ -29,17 +29,20 @@
 // would exceed 2^8.75, the range of e4m3.
 //
 // What bounds it, and what it measured.  64 requests of 2048 tokens, 128 heads on one latent head of
-// 576 + 512 (two groups of 64 heads read each row, one from L2): 69 us, where 75 MB of rows and
+// 576 + 512 (two groups of 64 heads read each row, one from L2): 68 us, where 75 MB of rows and
 // three 8-bit products a row would allow 19.  A CTA turns a tile of 96 tokens in 5000 cycles: its shared
 // memory has room for two tiles beside the 80 KB of q, so a tile's copy (2000 cycles at the
 // 27 B/cycle that 16-byte copies reach on an SM), scores (1150), softmax (2000) and values (1150) overlap
 // only with one other tile's.  With few rows the fixed parts count: 8 requests and 64 heads take 16 us,
 // 6 of them before the first scores (launch, look-up, first rows, cold instructions) and 2 joining
-// clusters; one request of 64 tokens 7.4 us.  16 requests of 8 heads of 128, 32 query heads, 2048
-// tokens (67 MB): 22 us, 3 TB/s.
+// clusters; one request of 64 tokens 7.3 us.  16 requests of 8 heads of 128, 32 query heads, 2048
+// tokens (67 MB): 20 us, 3.3 TB/s; there a tile's softmax is a chain of waits of one warp a
+// scheduler, 1300 cycles.
 // Not kept: rows gathered by the copy engine, four an instruction (100 us where the copies by threads
 // took 100 too); rows prefetched into L2 by the look-up warps (10,000 cycles a tile there); a barrier
-// for each 128 columns of a tile (116 us against 86).
+// for each 128 columns of a tile (116 us against 86); two softmax groups on alternate tiles (20 warps of
+// 96 registers spill, 27 us for the last case; 16 warps leave two to look rows up, 26 us); values before
+// scores, or scores before values, by a flag between the two warps (78 and 81 us).
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -1245,7 +1248,7 @@ struct Plan {
 // and the 7,400 cycles from a free stage to the next over the number of stages.  Wider groups read a row
 // fewer times, narrower ones make more CTAs.  For 8 requests of 2048 tokens and 64 heads that
 // reads, against what was measured (us): 16 heads by 4 CTAs 15 (16), 32 by 4 22 (22), 64 by 8
-// 20 (22), 16 by 1 32 (36); for 64 requests of 128 heads: 64 heads by 1 51 (69), 32 by 1 99 (108),
+// 20 (22), 16 by 1 32 (36); for 64 requests of 128 heads: 64 heads by 1 51 (68), 32 by 1 99 (108),
 // 16 by 1 129 (152).
 template <class T, int N>
 int plan_attend(const AttendArgs &args, int64_t pairs, Plan &best) {
