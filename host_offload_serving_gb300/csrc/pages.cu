@@ -153,8 +153,8 @@ __device__ void list_free(const PoolArgs &a, const Slice &s, const Words &w, uin
 // ---------------------------------------------------------------------------
 // Grow and fork.  Demands of the list's entries -> ranks -> free pages -> tables.  Bound by the
 // latency of about eight dependent reads of L2 and three cluster barriers: a fork of 32 in a pool of 4096 pages takes
-// 12 us with its copy; 40 requests freed and 40 grown by up to 1024 blocks in 200,003 pages 21 us
-// (33 with 32 pages to a thread in place of a word of 32 to a warp, 43 with four).
+// 12 us with its copy; 40 requests freed and 40 grown by up to 1024 blocks in 200,003 pages 18 us (21
+// with one warp to a request, 33 with 32 pages to a thread in place of a word of 32 to a warp too).
 // ---------------------------------------------------------------------------
 struct ForkNeed {
   bool ok;
@@ -172,16 +172,120 @@ __device__ __forceinline__ ForkNeed fork_need(const PoolArgs &a, int i) {
   return f;
 }
 
+// Blocks [lo, hi) of `total` for warp `part` of the `parts` of an entry.
+__device__ __forceinline__ Slice part_of(int total, int part, int parts) {
+  const int per = ((total + parts - 1) / parts + 31) & ~31;
+  const int lo = min(total, part * per);
+  return {lo, min(total, lo + per)};
+}
+// What entry i asks for, as far as this warp's part of it goes; INT_MIN: it is skipped.
+template <bool kFork>
+__device__ int demand_of(const PoolArgs &a, int i, int part, int parts) {
+  const int lane = threadIdx.x & 31;
+  if (kFork) {
+    const ForkNeed f = fork_need(a, i);
+    bool empty = f.ok;
+    if (f.ok) {
+      const int32_t *row = a.tables + static_cast<int64_t>(a.dst[i]) * a.blocks;
+      const Slice s = part_of(a.blocks, part, parts);
+#pragma unroll 8
+      for (int b = s.lo + lane; b < s.hi; b += 32) empty &= row[b] == -1;
+    }
+    if (!__all_sync(0xffffffffu, empty)) return INT_MIN;
+    return part == 0 && f.last >= 0 ? 1 : 0;
+  }
+  const int r = a.src[i], w = a.want[i];
+  if (r < 0 || r >= a.R || w < 0 || w > a.blocks) return INT_MIN;
+  const int32_t *row = a.tables + static_cast<int64_t>(r) * a.blocks;
+  const Slice s = part_of(w, part, parts);
+  int k = 0;
+#pragma unroll 8
+  for (int b = s.lo + lane; b < s.hi; b += 32) k += row[b] == -1;
+  return __reduce_add_sync(0xffffffffu, k);
+}
+// A fork's shared blocks, as far as this part goes; part 0 gives it the new last page, if it needs
+// one, and notes the rows to copy.
+__device__ void fork_entry(const PoolArgs &a, int i, int part, int parts, int need, int r0, const int32_t *to,
+                           int32_t *from, int32_t *rows_of) {
+  const int lane = threadIdx.x & 31;
+  int rows = 0, last = -1;
+  if (need >= 0 && r0 >= 0) {
+    const ForkNeed f = fork_need(a, i);
+    const int32_t *src = a.tables + static_cast<int64_t>(a.src[i]) * a.blocks;
+    int32_t *dst = a.tables + static_cast<int64_t>(a.dst[i]) * a.blocks;
+    const Slice s = part_of(f.full, part, parts);
+    for (int b = s.lo + lane; b < s.hi; b += 32) {
+      const int p = src[b];
+      if (p >= 0 && p < a.pages) {
+        dst[b] = p;
+        atomicAdd(a.refs + p, 1);
+      } else if (p != -1) {
+        report(a, HISPARSE_ERR_RANGE);
+      }
+    }
+    if (part == 0 && need && f.last >= a.pages) {
+      report(a, HISPARSE_ERR_RANGE);
+    } else if (part == 0 && need) {
+      rows = f.part;
+      last = f.last;
+      if (lane == 0) {
+        dst[f.full] = to[r0];
+        a.refs[to[r0]] = 1;
+      }
+    }
+  } else if (need >= 0 && part == 0 && lane == 0) {
+    report(a, HISPARSE_ERR_FULL);
+  }
+  // copy i: `rows` rows (0: none) of page `last`
+  if (part == 0 && lane == 0) {
+    rows_of[i] = rows;
+    from[i] = last;
+  }
+}
+// The pages of rank r ... for the holes of this part of a request's blocks.
+__device__ void grow_entry(const PoolArgs &a, int i, int part, int parts, int r, const int32_t *to) {
+  const int lane = threadIdx.x & 31;
+  int32_t *row = a.tables + static_cast<int64_t>(a.src[i]) * a.blocks;
+  const Slice s = part_of(a.want[i], part, parts);
+  for (int b0 = s.lo; b0 < s.hi; b0 += 8 * 32) {
+    bool hole[8];
+    int at[8], page[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int b = b0 + 32 * u + lane;
+      hole[u] = b < s.hi && row[b] == -1;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const unsigned m = __ballot_sync(0xffffffffu, hole[u]);
+      at[u] = r + __popc(m & ((1u << lane) - 1));
+      r += __popc(m);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) page[u] = hole[u] ? to[at[u]] : 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (hole[u]) {
+        row[b0 + 32 * u + lane] = page[u];
+        a.refs[page[u]] = 1;
+      }
+  }
+}
+
 template <bool kFork>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
-  __shared__ int warp_sums[32], slot[kPlanCtas];
+  __shared__ int warp_sums[32], slot[kPlanCtas], s_part[kPlanWarps];
   pdl_wait();
   pdl_launch();
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = cluster.block_rank(), lane = threadIdx.x & 31;
-  const int gwarp = (threadIdx.x >> 5) * kPlanCtas + rank;  // a short list goes over all CTAs
+  const int rank = cluster.block_rank(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kGWarps = kPlanCtas * kPlanWarps;
   int32_t *from = a.work + kWorkHead, *to = from + a.span, *third = to + a.span;
+  // An entry has `parts` warps of one CTA, where its blocks give each four for a lane and the whole
+  // list has warps at once; the list goes over all CTAs.
+  int parts = 8;
+  while (parts > 1 && (a.n * parts > kGWarps || 128 * parts > a.blocks)) parts >>= 1;
+  const int first = warp / parts * kPlanCtas + rank, part = warp % parts;
 
   cluster.barrier_arrive();  // (every CTA runs before another writes its shared memory)
   const Slice slice = slice_of(a.pages, rank);
@@ -190,29 +294,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
   int total;
   block_scan(count_free(a, slice, words, bits), warp_sums, total);
   // demand of each entry; INT_MIN marks one that is skipped
-  for (int i = gwarp; i < a.n; i += kGWarps) {
-    int need = INT_MIN;
-    if (kFork) {
-      const ForkNeed f = fork_need(a, i);
-      bool empty = f.ok;
-      if (f.ok) {
-        const int32_t *row = a.tables + static_cast<int64_t>(a.dst[i]) * a.blocks;
-#pragma unroll 8
-        for (int b = lane; b < a.blocks; b += 32) empty &= row[b] == -1;
-      }
-      if (__all_sync(0xffffffffu, empty)) need = f.last >= 0 ? 1 : 0;
-    } else {
-      const int r = a.src[i], w = a.want[i];
-      if (r >= 0 && r < a.R && w >= 0 && w <= a.blocks) {
-        const int32_t *row = a.tables + static_cast<int64_t>(r) * a.blocks;
-        int k = 0;
-#pragma unroll 8
-        for (int b = lane; b < w; b += 32) k += row[b] == -1;
-        need = __reduce_add_sync(0xffffffffu, k);
-      }
-    }
-    if (lane == 0) {
+  for (int i = first; i < a.n; i += kGWarps) {
+    const int need = demand_of<kFork>(a, i, part, parts);
+    if (lane == 0) s_part[warp] = need;
+    if (parts == 1 && lane == 0) {
       third[i] = need;
+      if (need == INT_MIN) report(a, HISPARSE_ERR_RANGE);
+    }
+  }
+  if (parts > 1) {  // (one turn of the loop above)
+    __syncthreads();
+    if (lane == 0 && part == 0 && first < a.n) {
+      int need = 0;
+      for (int p = 0; p < parts; ++p) need = need == INT_MIN || s_part[warp + p] == INT_MIN ? INT_MIN : need + s_part[warp + p];
+      third[first] = need;
       if (need == INT_MIN) report(a, HISPARSE_ERR_RANGE);
     }
   }
@@ -237,76 +332,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
   }
   cluster.sync();  // the free list, the ranks; everyone has read every demand
   if (kFork) {
-    for (int i = gwarp; i < a.n; i += kGWarps) {
-      const int need = third[i], r0 = from[i];
-      int rows = 0, last = -1;
-      if (need >= 0 && r0 >= 0) {
-        const ForkNeed f = fork_need(a, i);
-        const int32_t *src = a.tables + static_cast<int64_t>(a.src[i]) * a.blocks;
-        int32_t *dst = a.tables + static_cast<int64_t>(a.dst[i]) * a.blocks;
-        for (int b = lane; b < f.full; b += 32) {
-          const int p = src[b];
-          if (p >= 0 && p < a.pages) {
-            dst[b] = p;
-            atomicAdd(a.refs + p, 1);
-          } else if (p != -1) {
-            report(a, HISPARSE_ERR_RANGE);
-          }
-        }
-        if (need && f.last >= a.pages) {
-          report(a, HISPARSE_ERR_RANGE);
-        } else if (need) {
-          rows = f.part;
-          last = f.last;
-          if (lane == 0) {
-            dst[f.full] = to[r0];
-            a.refs[to[r0]] = 1;
-          }
-        }
-      } else if (need >= 0 && lane == 0) {
-        report(a, HISPARSE_ERR_FULL);
-      }
-      __syncwarp();
-      // copy i: `rows` rows (0: none) of page `last`
-      if (lane == 0) {
-        third[i] = rows;
-        from[i] = last;
-      }
+    int need = first < a.n ? third[first] : 0, r0 = first < a.n ? from[first] : 0;
+    if (parts > 1) __syncthreads();  // part 0 writes over what the others have read here
+    for (int i = first; i < a.n; i += kGWarps) {
+      if (i != first) need = third[i], r0 = from[i];
+      fork_entry(a, i, part, parts, need, r0, to, from, third);
     }
   } else {
-    for (int i = gwarp; i < a.n; i += kGWarps) {
+    for (int i = first; i < a.n; i += kGWarps) {
       const int need = third[i];
       int r = from[i];
       if (need <= 0) continue;
       if (r < 0) {
-        if (lane == 0) report(a, HISPARSE_ERR_FULL);
+        if (lane == 0 && part == 0) report(a, HISPARSE_ERR_FULL);
         continue;
       }
-      int32_t *row = a.tables + static_cast<int64_t>(a.src[i]) * a.blocks;
-      const int w = a.want[i];
-      for (int b0 = 0; b0 < w; b0 += 8 * 32) {
-        bool hole[8];
-        int at[8], page[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int b = b0 + 32 * u + lane;
-          hole[u] = b < w && row[b] == -1;
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const unsigned m = __ballot_sync(0xffffffffu, hole[u]);
-          at[u] = r + __popc(m & ((1u << lane) - 1));
-          r += __popc(m);
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) page[u] = hole[u] ? to[at[u]] : 0;
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (hole[u]) {
-            row[b0 + 32 * u + lane] = page[u];
-            a.refs[page[u]] = 1;
-          }
-      }
+      for (int p = 0; p < part; ++p) r += s_part[warp - part + p];
+      grow_entry(a, i, part, parts, r, to);
     }
   }
 }

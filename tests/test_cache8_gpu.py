@@ -684,6 +684,16 @@ def test_pages_random_life(pages_, R, M, bt, layers, row, seed):
         _same(pool, model, st)
 
 
+@pytest.mark.parametrize("pages_,R,M,bt,layers,row,seed", [
+    (20011, 24, 1300, 2, 1, 16, 7), (3000, 9, 2047, 1, 2, 16, 8), (70001, 100, 700, 1, 1, 16, 9),
+    (33000, 41, 1024, 1, 1, 16, 10),
+])
+def test_pages_long_tables(pages_, R, M, bt, layers, row, seed):
+    """The same with tables so long that an entry has 2, 4 or 8 warps, each with its own part
+    of the blocks; odd lengths, and a pool that runs out."""
+    test_pages_random_life(pages_, R, M, bt, layers, row, seed)
+
+
 def test_pages_refusals_on_the_device():
     """Bad indices and a destination that holds pages are skipped and reported."""
     model = PageModel(32, 5, 4, 8, 2, 16, 1)
