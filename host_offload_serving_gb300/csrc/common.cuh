@@ -151,6 +151,7 @@ __device__ __forceinline__ float2 rotary_cos_sin(int32_t position, int64_t turns
   const int64_t phase = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(position)) *
                                              static_cast<uint64_t>(turns));
   float s, c;
-  sincospif(static_cast<float>(phase) * 0x1p-63f, &s, &c);  // half turns in [-1, 1]
+  // (half turns in [-1, 1); the 32 bits left out are below 2^-31 of one, 32-bit results are not as fine)
+  sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &s, &c);
   return make_float2(c * amplitude, s * amplitude * sign);
 }

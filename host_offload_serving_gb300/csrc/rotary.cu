@@ -249,7 +249,7 @@ struct PackArgs {
   const int32_t *pages;
   int32_t max_blocks, page_tokens;
   int32_t rot, rot_offset, interleaved;
-  FastDiv half;
+  FastDiv half, by_S, by_team, by_heads;
   float amplitude, sign;
   const int64_t *turns;
   uint32_t *status;
@@ -276,7 +276,7 @@ __device__ __forceinline__ float2 turned(float2 a, float2 b) {  // a * b as comp
 // 32 bits than the sine's own).
 // Its bytes, 2 (or 4) read and 1 written a value, would allow half the time; what binds is the
 // instructions (about 20 a value, 2.6 issued a cycle) and the wait of each CTA for its one round of
-// loads.  8 ragged prompts of up to 4096 tokens, 8 + 8 heads of 128 (151 MB) take 45 us, 3.4 TB/s: with
+// loads.  8 ragged prompts of up to 4096 tokens, 8 + 8 heads of 128 (151 MB) take 44 us, 3.4 TB/s: with
 // 4 units a thread and 3 CTAs of 256 threads to an SM (80 registers); 2 units and 2 CTAs of 512 took
 // 53, 1 unit 79, 4 units and 6 CTAs of 128 49.  A sine for every token and pair, and the rotation
 // done twice in place of held, took 105.
@@ -300,14 +300,14 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) pack_kernel(const Pack
     return;
   }
   // The CTA's blocks and tokens, then this thread's team's.
-  const uint32_t blk0 = static_cast<uint32_t>(p0) / a.S + blockIdx.x * a.blocks_cta;
+  const uint32_t blk0 = a.by_S.div(p0) + blockIdx.x * a.blocks_cta;
   const int64_t stop = p0 + len;
   const int64_t cta_base = static_cast<int64_t>(blk0) * a.S;
   const int64_t cta_first = max(cta_base, static_cast<int64_t>(p0));
   if (cta_first >= stop) return;
   const int cta_tokens = static_cast<int>(min(cta_base + static_cast<int64_t>(a.blocks_cta) * a.S, stop) - cta_first);
-  const int team = threadIdx.x / a.team, tid = threadIdx.x - team * a.team;
-  const int group = team / a.heads;
+  const int team = a.by_team.div(threadIdx.x), tid = threadIdx.x - team * a.team;
+  const int group = a.by_heads.div(team);
   const bool is_v = static_cast<int>(blockIdx.z) >= a.k_groups;
   const int head = (is_v ? blockIdx.z - a.k_groups : blockIdx.z) * a.heads + (team - group * a.heads);
   const uint32_t blk = blk0 + group;
@@ -494,6 +494,9 @@ int launch_pack(PackArgs a, int span, int most, void *stream) {
   }
   const int tokens = a.blocks_cta > 1 ? std::min(a.blocks_cta * a.S, a.max_len) : std::min(a.side[0].abreast * PU, most);
   const int table = a.rot ? (kLow + (tokens + kLow - 1) / kLow) * (a.rot / 2) * static_cast<int>(sizeof(float2)) : 0;
+  a.by_S = FastDiv(a.S);
+  a.by_team = FastDiv(a.team);
+  a.by_heads = FastDiv(a.heads);
   a.k_groups = (a.kv_heads + a.heads - 1) / a.heads;
   return launch_pdl(pack_kernel<T, PU, THREADS, WALK>, dim3((span + a.blocks_cta - 1) / a.blocks_cta, a.n, a.k_groups * sides),
                     dim3((a.team * a.heads * a.blocks_cta + 31) / 32 * 32), table, stream, 1, a);
