@@ -89,6 +89,16 @@ def test_rotary(T, heads, k_heads, dim, rot, offset, interleaved, dtype):
         assert torch.equal(z, y)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("T,heads,k_heads,dim,rot,offset,interleaved", [
+    (2501, 12, 3, 64, 64, 0, False), (1500, 33, 1, 128, 64, 32, True), (3, 1, 1, 8192, 8192, 0, False),
+    (2, 1, 0, 8192, 8192, 0, True), (4099, 1, 0, 16, 8, 4, True), (700, 5, 5, 20, 12, 4, False),
+])
+def test_rotary_many_tokens(T, heads, k_heads, dim, rot, offset, interleaved, dtype):
+    """Several tokens and CTAs for a thread's unit, and the widest rotated part."""
+    test_rotary(T, heads, k_heads, dim, rot, offset, interleaved, dtype)
+
+
 def test_rotary_strided_views_and_untouched_rest():
     """A part of wider heads, by views whose strides and alignment are odd."""
     g = _gen(5)
@@ -226,6 +236,39 @@ def test_pack_by_position(rec, dtype, rot):
         seen[r, start[i]:start[i] + lens[i]] = True
     _pack_close(torch.cat(rows), want)
     assert (dst.cpu()[~seen] == 0x55).all()
+
+
+@pytest.mark.parametrize("rec,lens,rot,offset,interleaved,dtype", [
+    (cache8.Records(8, 64, 64, 1), [600, 3, 450, 599], 64, 0, True, torch.bfloat16),    # blocks of a token
+    (cache8.Records(4, 128, 128, 16), [900, 701, 17, 640], 32, 8, False, torch.float16),
+    (cache8.Records(5, 48, 80, 16), [333, 800], 16, 16, True, torch.float32),           # 5 heads, odd sizes
+    (cache8.Records(2, 192, 128, 64), [400, 33, 64, 1], 64, 128, False, torch.bfloat16),
+    (cache8.Records(1, 640, 512, 64, latent=True), [70, 131], 640, 0, False, torch.bfloat16),
+    (cache8.Records(1, 640, 512, 128, latent=True), [129, 300], 320, 160, True, torch.float32),
+    (cache8.Records(1, 16, 16, 4096), [5003, 4100], 16, 0, False, torch.bfloat16),      # blocks walked in parts
+    (cache8.Records(3, 512, 16, 200), [900], 128, 256, True, torch.float16),
+    (cache8.Records(17, 32, 16, 8), [90, 1, 64], 32, 0, False, torch.bfloat16),
+])
+def test_pack_blocks_and_heads_of_every_size(rec, lens, rot, offset, interleaved, dtype):
+    """Blocks of one token to thousands, one head to many, the rotated part anywhere in the head."""
+    g = _gen(sum(lens) + rot)
+    n = len(lens)
+    start = [(7 * i + 5) % (2 * rec.block_tokens) for i in range(n)]
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    k = (_randn(g, cu[-1], rec.kv_heads, rec.k_dim) * 2).to(dtype)
+    v = None if rec.latent else _randn(g, cu[-1], rec.kv_heads, rec.v_dim).to(dtype)
+    P = max(s + l for s, l in zip(start, lens))
+    scales = torch.zeros(n, rec.blocks(P), rec.columns, device="cuda")
+    turns = cache8.rotary_turns(rot)[0]
+    want, want_s = _pack64(rec, k, v, scales, start, cu, list(range(n)), 2.0, turns, offset, interleaved)
+    dst = torch.zeros(n, P, rec.row_bytes, dtype=torch.uint8, device="cuda")
+    st = _status()
+    cache8.pack(rec, k, v, dst, scales, torch.tensor(start, dtype=torch.int32, device="cuda"),
+                cu_lens=torch.tensor(cu, dtype=torch.int32, device="cuda"), max_len=max(lens), turns=turns.cuda(),
+                rot_offset=offset, interleaved=interleaved, status=st)
+    assert int(st) == 0
+    np.testing.assert_allclose(scales.double().cpu().numpy(), want_s, rtol=4e-6)
+    _pack_close(torch.cat([dst[i, start[i]:start[i] + lens[i]] for i in range(n)]), want)
 
 
 @pytest.mark.parametrize("rec", PACK_RECORDS[:3], ids=["latent", "heads", "odd"])
