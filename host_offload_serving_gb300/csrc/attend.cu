@@ -29,11 +29,11 @@
 // would exceed 2^8.75, the range of e4m3.
 //
 // What bounds it, and what it measured.  64 requests of 2048 tokens, 128 heads on one latent head of
-// 576 + 512 (two groups of 64 heads read each row, one from L2): 68 us, where 75 MB of rows and
-// three 8-bit products a row would allow 19.  A CTA turns a tile of 96 tokens in 5000 cycles: its shared
+// 576 + 512 (two groups of 64 heads read each row, one from L2): 66 us, where 75 MB of rows and
+// three 8-bit products a row would allow 19.  A CTA turns a tile of 96 tokens in 4500 cycles: its shared
 // memory has room for two tiles beside the 80 KB of q, so a tile's copy (2000 cycles at the
 // 27 B/cycle that 16-byte copies reach on an SM), scores (1150), softmax (2000) and values (1150) overlap
-// only with one other tile's.  With few rows the fixed parts count: 8 requests and 64 heads take 16 us,
+// only with one other tile's.  With few rows the fixed parts count: 8 requests and 64 heads take 15 us,
 // 6 of them before the first scores (launch, look-up, first rows, cold instructions) and 2 joining
 // clusters; one request of 64 tokens 7.3 us.  16 requests of 8 heads of 128, 32 query heads, 2048
 // tokens (67 MB): 20 us, 3.3 TB/s; there a tile's softmax is a chain of waits of one warp a
@@ -401,14 +401,15 @@ __device__ __forceinline__ void gather_columns(uint32_t table, uint32_t off, uin
 }
 
 // A tile's columns come, are multiplied and go in two halves: the chunks of K and of V, or those
-// of a latent record in two.  Chunks [c0, c1) of K or V; the values read [v0, v1) of them.
+// of a latent record in two of about as many 16-byte columns (16 and 20 of 36: 66 us for the largest case,
+// 24 and 12 68).  Chunks [c0, c1) of K or V; the values read [v0, v1) of them.
 struct Half {
   int c0, c1, v0, v1;
   bool is_v, scores;
 };
 __device__ __forceinline__ Half half_of(const AttendArgs &a, int u) {
   if (!a.latent) return {0, u ? a.v_chunks : a.k_chunks, 0, u ? a.v_chunks : 0, u == 1, u == 0};
-  const int mid = (a.k_chunks + 1) >> 1, c0 = u ? mid : 0, c1 = u ? a.k_chunks : mid;
+  const int mid = max(1, ((a.k_dim >> 4) + 8) >> 4), c0 = u ? mid : 0, c1 = u ? a.k_chunks : mid;
   return {c0, c1, min(c0, a.v_tiles), min(c1, a.v_tiles), false, true};
 }
 
@@ -1248,7 +1249,7 @@ struct Plan {
 // and the 7,400 cycles from a free stage to the next over the number of stages.  Wider groups read a row
 // fewer times, narrower ones make more CTAs.  For 8 requests of 2048 tokens and 64 heads that
 // reads, against what was measured (us): 16 heads by 4 CTAs 15 (16), 32 by 4 22 (22), 64 by 8
-// 20 (22), 16 by 1 32 (36); for 64 requests of 128 heads: 64 heads by 1 51 (68), 32 by 1 99 (108),
+// 20 (22), 16 by 1 32 (36); for 64 requests of 128 heads: 64 heads by 1 51 (66), 32 by 1 99 (108),
 // 16 by 1 129 (152).
 template <class T, int N>
 int plan_attend(const AttendArgs &args, int64_t pairs, Plan &best) {
