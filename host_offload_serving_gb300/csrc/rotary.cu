@@ -389,7 +389,8 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) pack_kernel(const Pack
         x[j][e + 1] = p.y;
       }
       const int t = off + lane_t + j * sd.abreast;
-      if (turns && t - off + c0 < nt) {
+      // (threads left over beside the last unit have tokens past their chunk's table)
+      if (turns && mine && t - off + c0 < nt) {
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
           const float4 l = *reinterpret_cast<const float4 *>(low + ((e >> 1) * kLow + (t & (kLow - 1))) * 2 * units + 2 * unit);
