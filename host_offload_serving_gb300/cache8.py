@@ -10,7 +10,7 @@
 ``attend``        attention over the rows that a slot vector names
                   (``hisparse_attend``).
 
-Each call checks its tensors' types and shapes here and everything else in the
+Each call checks its tensors' types, shapes and places here and everything else in the
 C library, launches on the current stream (or ``stream``) and returns at once;
 none allocates, so all can be captured in a CUDA graph.  ``status`` (an int32
 tensor of one element, optional) collects the ERR_* bits of device-side inputs.
@@ -46,6 +46,30 @@ def _i32(t, what, numel=None):
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{what}: {numel} values expected, got {t.numel()}")
     return t.data_ptr()
+
+
+def _reach(what, first, *others):
+    """Raises unless the current CUDA device reads every tensor (or None) where it lies: on that
+    device, or in pinned host memory."""
+    dev = first.get_device()
+    if dev >= 0 and dev == torch.cuda.current_device():
+        for t in others:
+            if t is not None and t.get_device() != dev:
+                break
+        else:
+            return
+    for t in (first, *others):
+        if t is None or (t.is_cuda and t.get_device() == torch.cuda.current_device()) \
+                or (t.device.type == "cpu" and t.is_pinned()):
+            continue
+        raise ValueError(f"{what}: a tensor of shape {tuple(t.shape)} is on {t.device}; all are on the "
+                         "current CUDA device, or in pinned host memory")
+
+
+def _turns(turns, what):
+    if turns.dtype is not torch.int64 or not turns.is_contiguous():
+        raise ValueError(f"{what}: turns is a contiguous int64 tensor")
+    return turns.data_ptr()
 
 
 class Records:
@@ -130,11 +154,11 @@ def rotate(x, positions, turns, *, k=None, out=None, k_out=None, offset=0, inter
         k_out = k if k_out is None else k_out
         _need(k.dtype is x.dtype, "rotate: x and k are of one type")
         second = _rotary_tensor(k, k_out, tokens, "k")
-    if turns.dtype is not torch.int64 or not turns.is_contiguous():
-        raise ValueError("rotate: turns is a contiguous int64 tensor")
+    d_turns, d_pos = _turns(turns, "rotate"), _i32(positions, "rotate: positions", tokens)
+    _reach("rotate", x, positions, turns, out, k, k_out)
     flags = (H.ROTARY_INTERLEAVED if interleaved else 0) | (H.ROTARY_INVERSE if inverse else 0)
     a = H.pack_rotary(dtype, 2 * turns.numel(), offset, flags, tokens, amplitude,
-                      _i32(positions, "rotate: positions", tokens), turns.data_ptr(), *first, *second)
+                      d_pos, d_turns, *first, *second)
     H.check(H.hisparse_rotary(a, _stream(stream)), "hisparse_rotary")
     return out, k_out
 
@@ -187,11 +211,13 @@ def pack(rec, k, v, dst, scales, start, *, cu_lens=None, reqs=None, max_len=1, h
     rot = (0, 0, 0, 0.0, 0)
     if turns is not None:
         rot = (2 * turns.numel(), rot_offset, H.ROTARY_INTERLEAVED if interleaved else 0, amplitude,
-               turns.data_ptr())
-    a = H.pack_pack(*rec.c, dtype, n, max_len, R, cs[1], headroom, _i32(cu_lens, "pack: cu_lens", n + 1),
-                    _i32(start, "pack: start"), _i32(reqs, "pack: reqs", n), tokens, k.data_ptr(), v_ptr,
+               _turns(turns, "pack"))
+    lists = (_i32(cu_lens, "pack: cu_lens", n + 1), _i32(start, "pack: start"), _i32(reqs, "pack: reqs", n),
+             _i32(status, "pack: status"))
+    _reach("pack", k, v, dst, scales, start, cu_lens, reqs, blocks, turns, status)
+    a = H.pack_pack(*rec.c, dtype, n, max_len, R, cs[1], headroom, *lists[:3], tokens, k.data_ptr(), v_ptr,
                     ks[0], ks[1], vs[0], vs[1], scales.data_ptr(), ss[0], dst.data_ptr(), rows[-2], ds[-2],
-                    req_stride, table, max_blocks, page_tokens, *rot, _i32(status, "pack: status"))
+                    req_stride, table, max_blocks, page_tokens, *rot, lists[3])
     H.check(H.hisparse_pack(a, _stream(stream)), "hisparse_pack")
     return dst
 
@@ -235,11 +261,13 @@ def attend(rec, q, sel, slots, hot, scales, out, *, softmax_scale=None, lse=None
         raise ValueError("attend: scales are float32 [R][blocks][columns]")
     if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.shape != shape[:3]):
         raise ValueError("attend: lse is float32 [R][rows][heads]")
+    lists = (_i32(seq_lens, "attend: seq_lens", R), _i32(num_reqs, "attend: num_reqs", 1),
+             _i32(status, "attend: status"))
+    _reach("attend", q, sel, slots, hot, scales, out, lse, seq_lens, resident, num_reqs, status)
     a = H.pack_attend(*rec.c, dtype, R, rows, listed[1] // rows, heads, hot_shape[1] - 1, record_tokens,
                       sel_block_tokens, rec.k_dim ** -0.5 if softmax_scale is None else softmax_scale,
                       q.data_ptr(), qs[by], qs[2], out.data_ptr(), os[by], os[2],
                       0 if lse is None else lse.data_ptr(), d_sel, d_slots, hot.data_ptr(), hs[0], hs[1],
-                      *store, scales.data_ptr(), ss[0], cs[1], _i32(seq_lens, "attend: seq_lens", R),
-                      _i32(num_reqs, "attend: num_reqs", 1), _i32(status, "attend: status"))
+                      *store, scales.data_ptr(), ss[0], cs[1], *lists)
     H.check(H.hisparse_attend(a, _stream(stream)), "hisparse_attend")
     return out

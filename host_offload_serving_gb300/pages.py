@@ -8,7 +8,7 @@ Calls launch on the current stream (or ``stream``) and return at once.
 import torch
 
 from . import hisparse as H
-from .cache8 import _i32, _need
+from .cache8 import _i32, _need, _reach
 from .runtime import _stream
 
 
@@ -23,6 +23,7 @@ class PagePool:
         _need(store.dtype is torch.uint8 and store.dim() == 3 and store.stride(2) == 1
               and store.shape[2] % block_tokens == 0,
               "PagePool: store is uint8 [layers][pages][block_tokens * row_bytes]")
+        _need(store.is_cuda, "PagePool: store is on a CUDA device")
         pages = store.shape[1]
         if tables is None:
             tables = torch.full((requests, max_blocks), -1, dtype=torch.int32, device=store.device)
@@ -40,24 +41,30 @@ class PagePool:
                             _i32(refs, "PagePool: refs", pages), self.work.data_ptr(),
                             _i32(status, "PagePool: status"))
 
+    def _lists(self, what, *named):
+        """The addresses of a call's lists (int32, of one length) and that length, all of them and the
+        pool checked."""
+        n = named[0][1].numel()
+        found = [_i32(t, f"{what}: {name}", n) for name, t in named]
+        _reach(what, self.store, self.tables, self.refs, self.status, *(t for _, t in named))
+        return (*found, n)
+
     def grow(self, reqs, blocks, stream=None):
         """Pages for blocks 0 .. blocks[i]-1 of request reqs[i] (int32, device)."""
-        H.check(H.hisparse_pages_grow(self.c, _i32(reqs, "grow: reqs"),
-                                      _i32(blocks, "grow: blocks", reqs.numel()), reqs.numel(),
+        H.check(H.hisparse_pages_grow(self.c, *self._lists("grow", ("reqs", reqs), ("blocks", blocks)),
                                       _stream(stream)), "hisparse_pages_grow")
 
     def fork(self, src, dst, tokens, stream=None):
         """Request dst[i] becomes a copy of the first tokens[i] positions of src[i]."""
-        n = src.numel()
-        H.check(H.hisparse_pages_fork(self.c, _i32(src, "fork: src"), _i32(dst, "fork: dst", n),
-                                      _i32(tokens, "fork: tokens", n), n, _stream(stream)),
-                "hisparse_pages_fork")
+        H.check(H.hisparse_pages_fork(self.c, *self._lists("fork", ("src", src), ("dst", dst), ("tokens", tokens)),
+                                      _stream(stream)), "hisparse_pages_fork")
 
     def free(self, reqs, stream=None):
         """Release every page of the listed requests."""
-        H.check(H.hisparse_pages_free(self.c, _i32(reqs, "free: reqs"), reqs.numel(),
-                                      _stream(stream)), "hisparse_pages_free")
+        H.check(H.hisparse_pages_free(self.c, *self._lists("free", ("reqs", reqs)), _stream(stream)),
+                "hisparse_pages_free")
 
     def compact(self, stream=None):
         """Move the pages in use to the front of the store."""
+        _reach("compact", self.store, self.tables, self.refs, self.status)
         H.check(H.hisparse_pages_compact(self.c, _stream(stream)), "hisparse_pages_compact")

@@ -1,0 +1,41 @@
+"""What the 8-bit record operators refuse before a launch, beyond test_cache8_cpu.py."""
+import pytest
+import torch
+
+from host_offload_serving_gb300 import cache8, pages
+
+REC = cache8.Records(2, 64, 64, 16)
+TURNS = cache8.rotary_turns(32)[0]
+
+
+def _zeros(*shape, dtype=torch.int32):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def _pack(**kw):
+    k = _zeros(3, 2, 64, dtype=torch.bfloat16)
+    a = dict(k=k, v=k, dst=_zeros(3, 256, dtype=torch.uint8), scales=torch.zeros(1, 4, 4), start=_zeros(1),
+             max_len=3, stream=0)
+    a.update(kw)
+    return cache8.pack(REC, a.pop("k"), a.pop("v"), a.pop("dst"), a.pop("scales"), a.pop("start"), **a)
+
+
+def test_tensors_that_the_gpu_does_not_reach_are_refused():
+    """Pageable host tensors, the frequency table as rotary_turns returns it among them."""
+    x = _zeros(3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="is on cpu"):
+        cache8.rotate(x, _zeros(3), TURNS, stream=0)
+    with pytest.raises(ValueError, match="is on cpu"):
+        _pack()
+    q = _zeros(2, 1, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="is on cpu"):
+        cache8.attend(REC, q, _zeros(2, 8), _zeros(2, 8), _zeros(2, 17, 256, dtype=torch.uint8),
+                      torch.zeros(2, 4, 4), torch.zeros_like(q), stream=0)
+    with pytest.raises(ValueError, match="CUDA device"):
+        pages.PagePool(_zeros(1, 4, 64, dtype=torch.uint8), requests=2, max_blocks=2, block_tokens=4)
+
+
+def test_pack_checks_its_frequency_table():
+    for turns in (TURNS.int(), TURNS.float(), torch.cat([TURNS, TURNS])[::2]):
+        with pytest.raises(ValueError, match="turns"):
+            _pack(turns=turns)

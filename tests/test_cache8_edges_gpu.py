@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from host_offload_serving_gb300 import cache8
+from host_offload_serving_gb300 import cache8, pages
 from test_cache8_gpu import _gen, _pack64, _pack_close, _randn, _status
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +42,43 @@ def test_pack_blocks_walked_by_teams_with_threads_left_over(rec, rot):
     assert int(st) == 0
     np.testing.assert_allclose(scales.double().cpu().numpy(), want_s, rtol=4e-6)
     _pack_close(torch.cat([dst[i, start[i]:start[i] + lens[i]] for i in range(2)]), want)
+
+
+# ---------------------------------------------------------------------------------------------
+# where tensors lie
+# ---------------------------------------------------------------------------------------------
+def test_host_tensors_are_refused_and_pinned_rows_written():
+    """One pageable host tensor among device tensors is refused by every call; rows may go to
+    pinned host memory."""
+    g = _gen(1)
+    rec = cache8.Records(1, 64, 64, 16)
+    turns, pos = cache8.rotary_turns(32)[0], _i32([0, 1, 2])
+    x = _randn(g, 3, 1, 64)
+    for bad in (dict(turns=turns), dict(pos=pos.cpu()), dict(k=x.cpu()), dict(out=x.cpu())):
+        kw = dict(dict(pos=pos, turns=turns.cuda()), **bad)
+        with pytest.raises(ValueError, match="is on cpu"):
+            cache8.rotate(x, kw.pop("pos"), kw.pop("turns"), **kw)
+    scales, start = torch.zeros(1, 1, 2, device="cuda"), _i32([0])
+    dst = torch.zeros(3, 128, dtype=torch.uint8, device="cuda")
+    for bad in (dict(turns=turns), dict(start=start.cpu()), dict(cu_lens=_i32([0, 3]).cpu()), dict(dst=dst.cpu()),
+                dict(scales=scales.cpu()), dict(v=x.cpu()), dict(status=start.cpu())):
+        kw = dict(dict(v=x, dst=dst, scales=scales, start=start), **bad)
+        with pytest.raises(ValueError, match="is on cpu"):
+            cache8.pack(rec, x, kw.pop("v"), kw.pop("dst"), kw.pop("scales"), kw.pop("start"), max_len=3, **kw)
+    q, sel = _randn(g, 1, 1, 1, 64).bfloat16(), _i32([[0, 1, 2]])
+    for bad in (dict(sel=sel.cpu()), dict(slots=sel.cpu()), dict(hot=dst[None].cpu()), dict(out=q.cpu()),
+                dict(scales=scales.cpu()), dict(lse=torch.zeros(1, 1, 1)), dict(seq_lens=start.cpu()),
+                dict(resident=dst.cpu()), dict(num_reqs=start.cpu()), dict(status=start.cpu())):
+        kw = dict(dict(sel=sel, slots=sel, hot=dst[None], scales=scales, out=q.clone()), **bad)
+        with pytest.raises(ValueError, match="is on cpu"):
+            cache8.attend(rec, q, kw.pop("sel"), kw.pop("slots"), kw.pop("hot"), kw.pop("scales"), kw.pop("out"), **kw)
+    pool = pages.PagePool(dst.view(1, 3, 128), block_tokens=1, requests=2, max_blocks=2)
+    for call in (lambda: pool.grow(start.cpu(), start), lambda: pool.grow(start, start.cpu()),
+                 lambda: pool.fork(start, start.cpu(), start), lambda: pool.free(start.cpu())):
+        with pytest.raises(ValueError, match="is on cpu"):
+            call()
+    pinned = torch.zeros(3, 128, dtype=torch.uint8).pin_memory()
+    cache8.pack(rec, x, x, dst, scales, start, max_len=3)
+    cache8.pack(rec, x, x, pinned, scales, start, max_len=3)
+    torch.cuda.synchronize()
+    assert bool(dst.any()) and torch.equal(dst.cpu(), pinned)
