@@ -43,26 +43,27 @@ __device__ __forceinline__ void report(const PoolArgs &a, uint32_t bit) {
 }
 
 // Sum over the CTA and this thread's exclusive prefix; all threads call it.
-__device__ __forceinline__ int block_scan(int v, int *warp_sums, int &total) {
+template <class T>
+__device__ __forceinline__ T block_scan(T v, T *warp_sums, T &total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();
   if (lane == 31) warp_sums[w] = x;
   __syncthreads();
-  const int s = warp_sums[lane];  // kPlanWarps == 32
-  int t = s;
+  const T s = warp_sums[lane];  // kPlanWarps == 32
+  T t = s;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, t, o);
+    const T y = __shfl_up_sync(0xffffffffu, t, o);
     if (lane >= o) t += y;
   }
   total = __shfl_sync(0xffffffffu, t, 31);
-  const int before = __shfl_sync(0xffffffffu, t - s, w);
+  const T before = __shfl_sync(0xffffffffu, t - s, w);
   return before + x - v;
 }
 
@@ -275,6 +276,7 @@ __device__ void grow_entry(const PoolArgs &a, int i, int part, int parts, int r,
 template <bool kFork>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
   __shared__ int warp_sums[32], slot[kPlanCtas], s_part[kPlanWarps];
+  __shared__ long long wide_sums[32];
   pdl_wait();
   pdl_launch();
   cg::cluster_group cluster = cg::this_cluster();
@@ -314,20 +316,20 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
   cluster.barrier_wait();
   tell(total, slot);
   cluster.sync();
-  // every CTA ranks the whole list: thread t takes a run of entries
+  // every CTA ranks the whole list: thread t takes a run of entries (in 64 bits: a list may ask for
+  // more than 2^31 pages, and its first entries still get theirs)
   const int run = (a.n + kPlanThreads - 1) / kPlanThreads;
   const int i0 = min(a.n, static_cast<int>(threadIdx.x) * run), i1 = min(a.n, i0 + run);
-  int mine = 0;
+  long long mine = 0, demand;
   for (int i = i0; i < i1; ++i) mine += max(0, third[i]);
-  int demand;
-  int at = block_scan(mine, warp_sums, demand);
+  long long at = block_scan(mine, wide_sums, demand);
   int free_pages;
   const int before = learn(slot, free_pages);
-  list_free(a, slice, words, bits, before, min(demand, a.pages), to, warp_sums);
+  list_free(a, slice, words, bits, before, static_cast<int>(min(demand, static_cast<long long>(a.pages))), to, warp_sums);
   // the demands that fit are a prefix of the list; `from` keeps each entry's first rank
   for (int i = i0; i < i1; ++i) {
     const int need = max(0, third[i]);
-    if (rank == 0) from[i] = need > 0 && at + need > free_pages ? -1 : at;
+    if (rank == 0) from[i] = need > 0 && at + need > free_pages ? -1 : static_cast<int>(min(at, static_cast<long long>(INT_MAX)));
     at += need;
   }
   cluster.sync();  // the free list, the ranks; everyone has read every demand

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from host_offload_serving_gb300 import cache8, pages
+from host_offload_serving_gb300 import hisparse as H
 from test_cache8_gpu import _gen, _pack64, _pack_close, _randn, _status
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +83,23 @@ def test_host_tensors_are_refused_and_pinned_rows_written():
     cache8.pack(rec, x, x, pinned, scales, start, max_len=3)
     torch.cuda.synchronize()
     assert bool(dst.any()) and torch.equal(dst.cpu(), pinned)
+
+
+# ---------------------------------------------------------------------------------------------
+# pages
+# ---------------------------------------------------------------------------------------------
+def test_pages_grow_by_more_than_31_bits():
+    """A list that asks for more than 2^31 pages: the entries before the first that finds too few
+    get theirs, the others none."""
+    R, M, n = 8192, 262300, 100
+    assert 15 + (R - 2) * M > 2 ** 31
+    st = _status()
+    pool = pages.PagePool(torch.zeros(1, n, 16, dtype=torch.uint8, device="cuda"), block_tokens=1, requests=R,
+                          max_blocks=M, status=st)
+    want = torch.full((R,), M, dtype=torch.int32, device="cuda")
+    want[0], want[1] = 10, 5
+    pool.grow(torch.arange(R, dtype=torch.int32, device="cuda"), want)
+    assert int(st) == H.ERR_FULL
+    assert pool.tables[0, :11].tolist() == [*range(10), -1] and pool.tables[1, :6].tolist() == [*range(10, 15), -1]
+    assert pool.refs.tolist() == [1] * 15 + [0] * (n - 15)
+    assert int((pool.tables != -1).sum()) == 15
