@@ -529,7 +529,8 @@ int pool_args(const hisparse_page_pool *p, PoolArgs &a) {
       !aligned16(p->d_refs) || p->layer_stride % 16 || p->page_stride % 16 ||
       p->page_stride < p->row_bytes * p->page_tokens || p->layer_stride < 0)
     return HISPARSE_EINVAL;
-  if (p->num_pages > (1 << 30) || p->num_requests > 8192) return HISPARSE_EBOUND;
+  // (loops over a table row step by up to 2048 blocks in 32 bits)
+  if (p->num_pages > (1 << 30) || p->num_requests > 8192 || p->max_blocks > (1 << 30)) return HISPARSE_EBOUND;
   a = {};
   a.pages = p->num_pages; a.R = p->num_requests; a.blocks = p->max_blocks;
   a.page_tokens = p->page_tokens; a.layers = p->layers;

@@ -642,7 +642,8 @@ int hisparse_attend(const hisparse_attend_args *args, void *stream);
  * each page.  The caller owns all of it: counts start at 0 and tables at -1.
  * Calls on one pool are ordered by the caller (one stream, or events).  Free pages
  * are those with count 0; new pages are always the lowest free ones, in the
- * order of the call's list, so results do not depend on timing. */
+ * order of the call's list, so results do not depend on timing.  At most 8192 requests, 2^30 pages
+ * and 2^30 blocks (EBOUND). */
 typedef struct {
   int32_t num_pages, num_requests, max_blocks, page_tokens, layers;
   int64_t row_bytes;     /* multiple of 16 */
@@ -679,13 +680,13 @@ int hisparse_pages_fork(const hisparse_page_pool *p, const int32_t *d_src, const
                         const int32_t *d_tokens, int32_t n, void *stream);
 
 /* Release every page of the listed requests: their table rows become -1 and
- * the counts fall.  Errors: EINVAL, ECUDA. */
+ * the counts fall.  Errors: EINVAL, EBOUND, ECUDA. */
 int hisparse_pages_free(const hisparse_page_pool *p, const int32_t *d_reqs, int32_t n,
                         void *stream);
 
 /* Move the pages in use to the front of the store: with m pages in use, the
  * j-th of those at or above m moves to the j-th free page below m, in every
- * layer, and every table follows.  No other page moves.  Errors: EINVAL, ECUDA. */
+ * layer, and every table follows.  No other page moves.  Errors: EINVAL, EBOUND, ECUDA. */
 int hisparse_pages_compact(const hisparse_page_pool *p, void *stream);
 
 /* (Library calls.)

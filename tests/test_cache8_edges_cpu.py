@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from host_offload_serving_gb300 import cache8, pages
+from host_offload_serving_gb300 import hisparse as H
 
 REC = cache8.Records(2, 64, 64, 16)
 TURNS = cache8.rotary_turns(32)[0]
@@ -39,3 +40,12 @@ def test_pack_checks_its_frequency_table():
     for turns in (TURNS.int(), TURNS.float(), torch.cat([TURNS, TURNS])[::2]):
         with pytest.raises(ValueError, match="turns"):
             _pack(turns=turns)
+
+
+def test_pages_bound_on_blocks():
+    """Table rows so long that 32-bit loops over them would wrap."""
+    p = H.PagePool(8, 2, 2 ** 30 + 1, 16, 1, 64, 0x1000, 8 * 1024, 1024, 0x1000, 0x1000, 0x1000, None)
+    assert H.hisparse_pages_grow(p, 0x1000, 0x1000, 1, None) == H.EBOUND
+    assert H.hisparse_pages_fork(p, 0x1000, 0x1000, 0x1000, 1, None) == H.EBOUND
+    assert H.hisparse_pages_free(p, 0x1000, 1, None) == H.EBOUND
+    assert H.hisparse_pages_compact(p, None) == H.EBOUND
