@@ -237,7 +237,9 @@ __device__ void fork_entry(const PoolArgs &a, int i, int part, int parts, int ne
   } else if (need >= 0 && part == 0 && lane == 0) {
     report(a, HISPARSE_ERR_FULL);
   }
-  // copy i: `rows` rows (0: none) of page `last`
+  // copy i: `rows` rows (0: none) of page `last`, in the places that the warp's lanes have read
+  // this entry's demand and rank from
+  __syncwarp();
   if (part == 0 && lane == 0) {
     rows_of[i] = rows;
     from[i] = last;
