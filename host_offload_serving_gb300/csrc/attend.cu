@@ -108,15 +108,18 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {  // sus
 // Waits have a limit (seconds, against microseconds in use).  One that runs out sets
 // *fail, after which no wait of the CTA waits any more: every loop still makes
 // its turns, so barriers stay matched, TMEM is freed and the kernel ends, with
-// HISPARSE_ERR_WAIT in the status.
-__device__ __noinline__ void bar_wait_long(uint32_t bar, uint32_t parity, volatile int *fail) {
+// HISPARSE_ERR_WAIT in the status.  They return whether the phase came:
+// the warps that copy rows stop where it did not, as the addresses would be those of no row.
+__device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int *fail) {
   const long long start = clock64();
-  while (!bar_try(bar, parity) && !*fail) {
+  while (!*fail) {
+    if (bar_try(bar, parity)) return true;
     if (clock64() - start > (1ll << 30)) *fail = 1;
   }
+  return false;
 }
-__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile int *fail) {
-  if (!bar_try(bar, parity)) bar_wait_long(bar, parity, fail);
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *fail) {
+  return bar_try(bar, parity) || bar_wait_long(bar, parity, fail);
 }
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
   constexpr int kThreads = Shape<N>::threads;
   constexpr int kQ = kTerms * N;  // rows of Q: the terms of a head are N rows apart
   extern __shared__ char smem_raw[];
-  __shared__ uint64_t s_bars[4 * kMaxStages + 3 * kTables + 7];
+  __shared__ uint64_t s_bars[4 * kMaxStages + 3 * kTables + 9];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   __shared__ float s_l[N], s_d[N], s_wmax[4][N], s_w[N];
@@ -499,6 +502,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
   const uint32_t b_read = b_s + 40;  // a score buffer has been read
   const uint32_t b_tab = b_s + 56, b_meta = b_tab + 8 * kTables,
                  b_used = b_meta + 8 * kTables;  // addresses and scales: written; done with
+  const uint32_t b_done = b_used + 8 * kTables;  // after a wait that ran out: the products issued so far
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = a.cluster > 1 ? blockIdx.x % a.cluster : 0;
   const uint32_t unit = blockIdx.x / a.cluster;
@@ -519,6 +523,8 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       bar_init(b_meta + 8 * t, 32 * Shape<N>::looks);
       bar_init(b_used + 8 * t, 1);
     }
+    bar_init(b_done, 1);
+    bar_init(b_done + 8, 1);
     s_fail = 0;
   }
   for (int i = tid; i < 2 * a.stages; i += kThreads) {
@@ -809,12 +815,13 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     const uint32_t table = base + a.off_rows + (half.is_v ? kTables * a.tile * 8 : 0);
     uint32_t st = base + (half.is_v ? a.k_chunks * a.tile * 128 : 0);
     int s = 0, turn = 0;  // the tile's stage, and how often the stages went round
+    bool good = true;     // every table so far was written
     for (int i = 0; i < tiles; ++i) {
       const int groups = (min(a.tile, t1 - t0 - i * a.tile) + 31) >> 5 << 2;
       const uint32_t rows = table + i % kTables * a.tile * 8;
-      bar_wait(b_tab + 8 * (i % kTables), (i / kTables) & 1, fail);
-      if (turn > 0) bar_wait(b_empty + 16 * s + 8 * u, (turn - 1) & 1, fail);
-      for (int col0 = 8 * half.c0; col0 < cols;) {
+      good = bar_wait(b_tab + 8 * (i % kTables), (i / kTables) & 1, fail) && good;
+      if (turn > 0) good = bar_wait(b_empty + 16 * s + 8 * u, (turn - 1) & 1, fail) && good;
+      for (int col0 = good ? 8 * half.c0 : cols; col0 < cols;) {
         const int left = cols - col0, lw = left >= 32 ? 5 : 31 - __clz(left);
         const int j = col0 + (lane & ((1 << lw) - 1));
         const uint32_t dst = st + (j >> 3) * a.tile * 128 + ((j & 7) << 4);
@@ -1041,6 +1048,17 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
   const int share = N / a.cluster, n0 = static_cast<int>(rank) * share;
   if (!lone) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all CTAs run
   __syncthreads();
+  if (s_fail) {  // (no wait follows that sets it)  The products end before TMEM goes.
+    if (warp == Shape<N>::mma || warp == Shape<N>::mma + 1) {
+      const uint32_t bar = b_done + 8 * (warp - Shape<N>::mma);
+      if (elect_one()) tc_commit(bar);
+      __syncwarp();
+      const long long start = clock64();
+      while (!bar_try(bar, 0) && clock64() - start < (1ll << 30)) {
+      }
+    }
+    __syncthreads();
+  }
   T *out = static_cast<T *>(a.out) + qrow * a.out_row;
   const int h0 = kvh * a.group + hg * N, heads = min(N, a.group - static_cast<int>(hg) * N);
   if (!lone && tid < N) {  // a column's offset and sum to the CTA that joins it
