@@ -108,7 +108,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {  // sus
 // Waits have a limit (seconds, against microseconds in use).  One that runs out sets
 // *fail, after which no wait of the CTA waits any more: every loop still makes
 // its turns, so barriers stay matched, TMEM is freed and the kernel ends, with
-// HISPARSE_ERR_WAIT in the status.  They return whether the phase came:
+// HISPARSE_ERR_WAIT in the status and NaN in its outputs.  They return whether the phase came:
 // the warps that copy rows stop where it did not, as the addresses would be those of no row.
 __device__ __noinline__ bool bar_wait_long(uint32_t bar, uint32_t parity, volatile int *fail) {
   const long long start = clock64();
@@ -1048,7 +1048,8 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
   const int share = N / a.cluster, n0 = static_cast<int>(rank) * share;
   if (!lone) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // all CTAs run
   __syncthreads();
-  if (s_fail) {  // (no wait follows that sets it)  The products end before TMEM goes.
+  if (s_fail) {  // (no wait follows that sets it)  Nothing here is a result; the products end before TMEM goes.
+    if (tid < N) s_l[tid] = s_f[tid] = NAN;
     if (warp == Shape<N>::mma || warp == Shape<N>::mma + 1) {
       const uint32_t bar = b_done + 8 * (warp - Shape<N>::mma);
       if (elect_one()) tc_commit(bar);

@@ -629,7 +629,8 @@ typedef struct {
  * max(2^-8 p, 2^-16 of the row's largest) (f16: 2^-13, 2^-20).  A scale of V below 2^-100 counts as 2^-100.  A slot
  * outside what B, resident and -1 allow, or a selected position outside
  * the scale table or of 2^31 or more, sets HISPARSE_ERR_RANGE and is left out.
- * HISPARSE_ERR_WAIT: a wait inside the kernel ran out (it ends; its outputs do not count).
+ * HISPARSE_ERR_WAIT: a wait inside the kernel ran out (it ends, with NaN in out and lse of the rows
+ * concerned, whether or not there is a d_status).
  * Results do not depend on timing.  q, out, hot and resident are 16-byte aligned.
  * Errors: EINVAL; EBOUND (sizes of hisparse_records; more than 65535 heads, tokens of a record
  * or of a selected block; 2^28 rows of q; 2^30 tokens of a row; 2^31 scales of a request; row strides of
