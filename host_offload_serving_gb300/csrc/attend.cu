@@ -54,6 +54,7 @@ namespace {
 constexpr int kMaxStages = 6;
 constexpr int kMaxCluster = 16;
 constexpr float kNone = -1e30f; // a CTA's offset where it had no token
+constexpr int32_t kMasked = 0x7fffffff;  // in place of K's scale: a token that does not count
 // log2 of a column's largest probability when its offset is set, and what it may grow to before
 // the offset moves again (the largest e4m3 is 448 = 2^8.8).
 constexpr float kTop = 6.f, kSlack = 8.75f;
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
                      : "=f"(meta.x), "=f"(meta.y)
                      : "r"(base + a.off_meta + (i % kTables * a.tile + tk) * 8)
                      : "memory");
-        use = __float_as_int(meta.x) != 0x7fffffff;
+        use = __float_as_int(meta.x) != kMasked;
         if (use) {
           ks = meta.x;
           // (approximate to 2^-21, and the inverse of the very same)
@@ -894,6 +895,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     struct Step {
       Raw r;
       int32_t k, v;
+      bool use;
     };
     auto fetch = [&](Step &x, int tile, int sub) {
       const int j = mine + 32 * kLooks * sub;
@@ -901,9 +903,11 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     };
     auto put_scales = [&](const Step &x, int tile, int sub) {
       const int j = mine + 32 * kLooks * sub;
+      // a NaN scale of K may have the masked tokens' bits: it gets others
+      const int32_t k = !x.use ? kMasked : (x.k & 0x7fffffff) > 0x7f800000 ? 0x7fc00000 : x.k;
       if (j < a.tile)
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(base + a.off_meta + (tile % kTables * a.tile + j) * 8),
-                     "r"(x.k), "r"(x.v)
+                     "r"(k), "r"(x.v)
                      : "memory");
       if (sub == per - 1) bar_arrive(b_meta + 8 * (tile % kTables));
     };
@@ -936,8 +940,9 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
         advance(bt, bs);
       }
       const int32_t *sc = reinterpret_cast<const int32_t *>(now.scales);
-      x.k = ld_if(sc, now.row != 0, 0x7fffffff);
-      x.v = ld_if(sc + v_col, now.row != 0, 0);
+      x.use = now.row != 0;
+      x.k = ld_if(sc, x.use, 0);
+      x.v = ld_if(sc + v_col, x.use, 0);
     };
     Step x0, x1;
     fetch(x0, at, as), advance(at, as);

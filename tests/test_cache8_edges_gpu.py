@@ -7,7 +7,8 @@ import torch
 
 from host_offload_serving_gb300 import cache8, pages
 from host_offload_serving_gb300 import hisparse as H
-from test_cache8_gpu import _gen, _pack64, _pack_close, _randn, _status
+from test_cache8_gpu import (E4M3, HEADS, LATENT, PageModel, _attend, _attend64, _attend_case, _attend_close, _gen,
+                             _pack64, _pack_close, _randn, _rotated64, _same, _status)
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +104,51 @@ def test_pages_grow_by_more_than_31_bits():
     assert pool.tables[0, :11].tolist() == [*range(10), -1] and pool.tables[1, :6].tolist() == [*range(10, 15), -1]
     assert pool.refs.tolist() == [1] * 15 + [0] * (n - 15)
     assert int((pool.tables != -1).sum()) == 15
+
+
+# ---------------------------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------------------------
+def _bits(pattern):
+    return torch.tensor(pattern, dtype=torch.int32, device="cuda").view(torch.float32)
+
+
+@pytest.mark.parametrize("rec,heads", [(LATENT, 16), (HEADS, 16), (cache8.Records(2, 64, 64, 16), 64),
+                                       (cache8.Records(1, 128, 128, 16), 64)])
+@pytest.mark.parametrize("pattern", [0x7FFFFFFF, 0x7FC00000, -1])
+def test_attend_scales_of_k_that_are_nan(rec, heads, pattern):
+    """Whatever its bits, a NaN scale of K makes the rows that read it NaN, and no others."""
+    c = _attend_case(rec, heads, torch.bfloat16, 2, 1, 200, pad=0.1)
+    assert _attend(c) == 0
+    out, lse = c["out"].clone(), c["lse"].clone()
+    j = int((c["slots"][1] >= 0).nonzero()[100])
+    c["scales"][1, int(c["sel"][1, j]) // rec.block_tokens, rec.kv_heads - 1] = _bits(pattern)
+    assert _attend(c) == 0
+    hit = torch.zeros(2, 1, heads, dtype=torch.bool, device="cuda")
+    hit[1, 0, heads - heads // rec.kv_heads:] = True
+    assert bool(torch.isnan(c["out"][hit]).all()) and bool(torch.isnan(c["lse"][hit]).all())
+    assert torch.equal(c["out"][~hit], out[~hit]) and torch.equal(c["lse"][~hit], lse[~hit])
+
+
+def test_attend_infinite_scales_of_k():
+    """Scores of minus infinity have no weight; a score of plus infinity leaves no number."""
+    c = _attend_case(HEADS, 16, torch.bfloat16, 2, 1, 200, pad=0.1)
+    j = int((c["slots"][1] >= 0).nonzero()[100])
+    clean = c["scales"].clone()
+    blk = int(c["sel"][1, j]) // 16
+    same = (c["sel"][1] // 16 == blk) & (c["sel"][1] >= 0)
+    same[j] = False
+    c["sel"][1, same] = c["slots"][1, same] = -1           # the block's only token
+    c["scales"][1, blk, :4] = float("inf")
+    assert _attend(c) == 0
+    gone = c["slots"].clone()
+    gone[1, j] = -1
+    want = _attend64(HEADS, c["q"], c["sel"], gone, c["hot"], clean, 128 ** -0.5)
+    row = c["hot"][1, c["slots"][1, j]].view(E4M3).double()[:4 * 128].view(4, 128)
+    up = torch.einsum("hgd,hd->hg", c["q"][1, 0].double().view(4, 4, 128), row).view(16) > 0
+    low = torch.ones(2, 1, 16, dtype=torch.bool, device="cuda")
+    low[1, 0] = ~up
+    assert 0 < int(up.sum()) < 16
+    assert bool((~torch.isfinite(c["out"][~low])).all()) and bool((~torch.isfinite(c["lse"][~low])).all())
+    m = low.cpu().numpy()
+    _attend_close(c["out"][low][None, None], c["lse"][low][None, None], [x[m][None, None] for x in want], torch.bfloat16)
