@@ -636,12 +636,13 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       for (int c = 0; c < NC; ++c) qf[kHeld ? c : 0] = s_qf[c0 + c], off[kHeld ? c : 0] = 0.f;
     }
     // This lane's token of a tile: its scale of K, and of V as log2 and inverse.
+    // A scale of V that is no number leaves the softmax as it is and spoils the token's probabilities.
     float ks, lv, iv;
-    bool use;
+    bool use, spoilt;
     auto scales_of = [&](int i) {
       bar_wait(b_meta + 8 * (i % kTables), (i / kTables) & 1, fail);
       ks = 0.f, lv = 0.f, iv = 1.f;
-      use = false;
+      use = spoilt = false;
       if (tk < min(a.tile, t1 - t0 - i * a.tile)) {
         float2 meta;
         asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
@@ -651,8 +652,9 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
         use = __float_as_int(meta.x) != kMasked;
         if (use) {
           ks = meta.x;
+          spoilt = !(meta.y < INFINITY);
           // (approximate to 2^-21, and the inverse of the very same)
-          lv = lg2(fmaxf(meta.y, 0x1p-100f));
+          if (!spoilt) lv = lg2(fmaxf(meta.y, 0x1p-100f));
           iv = ex2(-lv);
         }
       }
@@ -758,6 +760,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       for (int c = 0; c < NC; ++c) {
         x[c] = ex2(x[c]);
         l[c] = fmaf(x[c], iv, l[c]);
+        if (spoilt) x[c] = NAN;
       }
       if (i + 1 < tiles) scales_of(i + 1);  // while the products before are still under way
       if (!moved) previous();

@@ -627,7 +627,8 @@ typedef struct {
  * cores as the e4m3 they are, q and the probabilities as sums of 8-bit terms, two for
  * bf16 and three for f16: q at least as fine as its type, a probability p within
  * max(2^-8 p, 2^-16 of the row's largest) (f16: 2^-13, 2^-20).  A scale of V below 2^-100 counts as 2^-100.
- * A NaN scale of K gives NaN in out and lse of the rows that read it.  A slot
+ * A NaN scale of K gives NaN in out and lse of the rows that read it; one of V that is NaN or
+ * infinite in out alone.  A slot
  * outside what B, resident and -1 allow, or a selected position outside
  * the scale table or of 2^31 or more, sets HISPARSE_ERR_RANGE and is left out.
  * HISPARSE_ERR_WAIT: a wait inside the kernel ran out (it ends, with NaN in out and lse of the rows

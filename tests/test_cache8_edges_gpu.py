@@ -130,6 +130,24 @@ def test_attend_scales_of_k_that_are_nan(rec, heads, pattern):
     assert torch.equal(c["out"][~hit], out[~hit]) and torch.equal(c["lse"][~hit], lse[~hit])
 
 
+@pytest.mark.parametrize("heads", [8, 16, 128, 256])
+@pytest.mark.parametrize("pattern", [0x7FFFFFFF, 0x7FC00000, 0x7F800000])
+def test_attend_scales_of_v_that_are_no_numbers(heads, pattern):
+    """... and one of V their outputs; the softmax and its lse have nothing of V in them."""
+    c = _attend_case(HEADS, heads, torch.bfloat16, 2, 1, 200, pad=0.1)
+    assert _attend(c) == 0
+    out = c["out"].clone()
+    want = _attend64(HEADS, c["q"], c["sel"], c["slots"], c["hot"], c["scales"], 128 ** -0.5)
+    j = int((c["slots"][1] >= 0).nonzero()[100])
+    c["scales"][1, int(c["sel"][1, j]) // 16, HEADS.columns - 1] = _bits(pattern)
+    assert _attend(c) == 0
+    hit = torch.zeros(2, 1, heads, dtype=torch.bool, device="cuda")
+    hit[1, 0, heads - heads // 4:] = True
+    assert bool((~torch.isfinite(c["out"][hit])).all())
+    assert torch.equal(c["out"][~hit], out[~hit])
+    _attend_close(out, c["lse"], want, torch.bfloat16)
+
+
 def test_attend_infinite_scales_of_k():
     """Scores of minus infinity have no weight; a score of plus infinity leaves no number."""
     c = _attend_case(HEADS, 16, torch.bfloat16, 2, 1, 200, pad=0.1)
