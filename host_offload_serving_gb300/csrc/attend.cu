@@ -10,34 +10,40 @@
 // Both run on the tensor cores (tcgen05.mma kind::f8f6f4, M = 128) with the
 // records' e4m3 bytes as they are: nothing is dequantised, and a latent record's K tile
 // serves as V without a second copy.  What is not 8 bits becomes a sum of 8-bit terms:
-// q, scaled by a power of two for each head, is t1 + t2 (+ t3 for f16), each the e4m3
-// rounding of what the ones before leave; bf16's 8 significant bits are two such terms
-// exactly.  The probabilities are e4m3 + e5m2 (f16: e4m3 + e4m3 + e5m2), the last term in e5m2 for
-// its range: each within 2^-8 (2^-13) of itself, or 2^-16 (2^-20) of the largest.  The errors of
-// a row's tokens are independent: with 2048 of them the output is 0.0019 from 64 bits' (root mean square,
-// relative), where rounding to bf16 alone gives 0.0017.  All sums are in 32 bits.
+// q, scaled by a power of two for each head to below 2^8, is t1 + t2 (+ t3 for f16), each the e4m3
+// rounding of what the ones before leave.  That is exact down to 2^-9 (f16: 2^-6) of the head's largest
+// value; e4m3 ends at 2^-9, so smaller ones are within 2^-17 of the largest.
 // The scale of K enters the scores in 32 bits; the scale of V enters the probabilities
 // (p_j sV_j is what multiplies the raw bytes of V), through the exponent, so the
 // running maximum is over s_j + log2(sV_j) and no product leaves the range.
+// The p_j sV_j are three e5m2 terms, four for f16: each leaves 2^-4 of what it rounds, so together
+// 2^-11 (2^-15), as far down as the last reaches, 2^-17 where the largest is 2^15.  Their range is what
+// counts where one token has nearly all of the weight and a small V: the output is then made
+// of the others, which lie 2^-20 below.  (e4m3 and e5m2, with the largest at 2^2 so that it could grow,
+// lost them: 3 % from 64 bits beside a token of weight 0.9, 40 % at 0.997; now 0.0017, which is the
+// rounding to bf16, up to 0.9999.)  All sums are in 32 bits.
 //
 // Warps: four softmax warps (a lane a token, TMEM lane = token) for each 32 columns; six (four for
 // 64 columns) that gather (16-byte cp.async into the 128-byte-swizzled tiles that the tensor cores
 // read, as many tiles ahead as there are stages); four (two) that turn slots and positions into
 // addresses and scales, further ahead; and two that issue the products.  S is double buffered in
 // TMEM, so the scores of tile i+1 are computed while the softmax of tile i runs.  A column's offset
-// is set so that its largest probability is 2^top, and moves (with its sums and O) only where one
-// would exceed 2^8.75, the range of e4m3.
+// moves (with its sums and O) only where a probability would exceed 2^15.75, the range of e5m2.  It is set
+// so that 2^12 of that are left above the largest of the warp that lies lowest, and the largest is 2^15 at most:
+// in rows of normal scores the largest of later tiles seldom passes that, and a dominant token gets the
+// whole range below it.  Of 16 requests of 2048 tokens: 21.8 us, 22.6 with 2^10 left and 23.9 with 2^8, 21.4
+// where nothing ever moves.
 //
 // What bounds it, and what it measured.  64 requests of 2048 tokens, 128 heads on one latent head of
-// 576 + 512 (two groups of 64 heads read each row, one from L2): 66 us, where 75 MB of rows and
-// three 8-bit products a row would allow 19.  A CTA turns a tile of 96 tokens in 4500 cycles: its shared
+// 576 + 512 (two groups of 64 heads read each row, one from L2): 76 us, where 75 MB of rows would allow 14
+// and the products (two terms with K, three with V) 26.  A CTA turns a tile of 96 tokens in 5100 cycles: its shared
 // memory has room for two tiles beside the 80 KB of q, so a tile's copy (2000 cycles at the
-// 27 B/cycle that 16-byte copies reach on an SM), scores (1150), softmax (2000) and values (1150) overlap
-// only with one other tile's.  With few rows the fixed parts count: 8 requests and 64 heads take 15 us,
-// 6 of them before the first scores (launch, look-up, first rows, cold instructions) and 2 joining
-// clusters; one request of 64 tokens 7.3 us.  16 requests of 8 heads of 128, 32 query heads, 2048
-// tokens (67 MB): 20 us, 3.3 TB/s; there a tile's softmax is a chain of waits of one warp a
-// scheduler, 1300 cycles.
+// 27 B/cycle that 16-byte copies reach on an SM), scores (1150), softmax (2000) and values (1730) overlap
+// only with one other tile's.  (The third product with V is 6 us of it.)  With few rows the fixed parts count: 8
+// requests and 64 heads take 16 us, 6 of them before the first scores (launch, look-up, first rows, cold
+// instructions) and 2 joining clusters; one request of 64 tokens 7.9 us.  16 requests of 8 heads of 128, 32
+// query heads, 2048 tokens (67 MB): 21.7 us, 3.2 TB/s; there a tile's softmax is a chain of waits of one
+// warp a scheduler, 1300 cycles.
 // Not kept: rows gathered by the copy engine, four an instruction (100 us where the copies by threads
 // took 100 too); rows prefetched into L2 by the look-up warps (10,000 cycles a tile there); a barrier
 // for each 128 columns of a tile (116 us against 86); two softmax groups on alternate tiles (20 warps of
@@ -55,9 +61,13 @@ constexpr int kMaxStages = 6;
 constexpr int kMaxCluster = 16;
 constexpr float kNone = -1e30f; // a CTA's offset where it had no token
 constexpr int32_t kMasked = 0x7fffffff;  // in place of K's scale: a token that does not count
-// log2 of a column's largest probability when its offset is set, and what it may grow to before
-// the offset moves again (the largest e4m3 is 448 = 2^8.8).
-constexpr float kTop = 6.f, kSlack = 8.75f;
+// log2 of a column's largest probability at the most when its offset is set, of what it may grow to
+// before the offset moves again (the largest e5m2 is 57344 = 2^15.8), the room that is left above the
+// warp whose tokens lie lowest, and the largest probability where only one warp has any.
+constexpr float kTop = 15.f, kSlack = 15.75f, kRoom = 12.f, kAlone = 9.f;
+// Sums of probabilities are kept 2^-kFold of what they are: a token whose scale of V is 2^-100 adds
+// 2^115 at the most, and a few thousand of them would leave the range.
+constexpr float kFold = 16.f;
 
 struct AttendArgs {
   int32_t rows, entries, heads, kv_heads, k_dim, v_dim, latent, B;
@@ -81,6 +91,7 @@ struct AttendArgs {
   uint32_t *status;
   // the launch's plan
   int32_t cluster, per_cta, tile, stages, k_chunks, v_chunks, v_tiles, tmem_cols;
+  int32_t sums;  // of a column: one, or one for each term of the probabilities
   FastDiv quads;  // v_dim / 4
   uint32_t stage_bytes, off_q, off_p, off_meta, off_rows;
 };
@@ -146,6 +157,8 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
 // bytes apart (either major-ness: the other offset is not used).  Its lower word; the
 // upper one is the same for all.
 constexpr uint32_t kDescHi = 64u | 1u << 14 | 2u << 29;
+// The same of one with 64-byte swizzle, whose groups of 8 rows are 512 bytes apart.
+constexpr uint32_t kDescHi64 = 32u | 1u << 14 | 4u << 29;
 __device__ __forceinline__ uint32_t smem_desc(uint32_t addr) { return addr >> 4 | 1u << 16; }
 // Instruction descriptor: f32 accumulator, A e4m3, B e4m3 or e5m2, M = 128.
 __device__ __forceinline__ uint32_t mma_desc(int n, bool b_e5m2, bool transposed) {
@@ -155,13 +168,14 @@ __device__ __forceinline__ uint32_t mma_desc(int n, bool b_e5m2, bool transposed
 // Products are issued by one lane, in unrolled runs of constant offsets: the operands go through
 // uniform registers, and a run of any length keeps the tensor cores fed (39 cycles an
 // instruction for 16 columns, 64 for 128), where a loop around one took 100.
+template <uint32_t kHiB = kDescHi>
 __device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 da, db;\n"
       " setp.ne.b32 p, %4, 0;\n"
-      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+      " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %6};\n"
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHi), "r"(kHiB)
       : "memory");
 }
 __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t *r) {
@@ -275,21 +289,33 @@ __device__ __forceinline__ void st_shared4(uint32_t addr, uint32_t x, uint32_t y
                : "memory");
 }
 
-// Two values to e4m3 (or e5m2) with rounding to nearest; *x and *y keep what the rounding
-// leaves.
-template <bool kE5M2>
+// Two values to e4m3 with rounding to nearest; *x and *y keep what the rounding leaves.
 __device__ __forceinline__ uint32_t take_term(float &x, float &y) {
   uint16_t p;
   uint32_t h;
-  if (kE5M2) {
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(p) : "f"(y), "f"(x));
-    return p;
-  }
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(y), "f"(x));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(p));
   const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
   x -= f.x;
   y -= f.y;
+  return p;
+}
+// Two values to e5m2, the upper byte of f16, with rounding to nearest; they keep what the rounding leaves,
+// exactly.
+__device__ __forceinline__ uint32_t take_e5m2(float &x, float &y) {
+  uint16_t p;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(p) : "f"(y), "f"(x));
+  const uint32_t back = __byte_perm(p, 0, 0x1404);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+  x -= f.x;
+  y -= f.y;
+  return p;
+}
+__device__ __forceinline__ uint32_t take_e5m2(__half2 &h) {
+  uint16_t p;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(p) : "r"(*reinterpret_cast<const uint32_t *>(&h)));
+  const uint32_t back = __byte_perm(p, 0, 0x1404);
+  h = __hsub2(h, *reinterpret_cast<const __half2 *>(&back));
   return p;
 }
 
@@ -357,10 +383,10 @@ __device__ __noinline__ Split<kTerms> split8(uint4 v, float up) {
     for (int j = 0; j < 8; ++j) x[j] = to_f32<T>(e[j]) * up;
 #pragma unroll
     for (int t = 0; t < kTerms; ++t) {
-      w0[t] = take_term<false>(x[0], x[1]);
-      w0[t] |= take_term<false>(x[2], x[3]) << 16;
-      w1[t] = take_term<false>(x[4], x[5]);
-      w1[t] |= take_term<false>(x[6], x[7]) << 16;
+      w0[t] = take_term(x[0], x[1]);
+      w0[t] |= take_term(x[2], x[3]) << 16;
+      w1[t] = take_term(x[4], x[5]);
+      w1[t] |= take_term(x[6], x[7]) << 16;
     }
   }
   return s;
@@ -409,12 +435,12 @@ __device__ __forceinline__ void gather_columns(uint32_t table, uint32_t off, uin
 // 24 and 12 68).  Chunks [c0, c1) of K or V; the values read [v0, v1) of them.
 struct Half {
   int c0, c1, v0, v1;
-  bool is_v, scores;
+  bool is_v;
 };
 __device__ __forceinline__ Half half_of(const AttendArgs &a, int u) {
-  if (!a.latent) return {0, u ? a.v_chunks : a.k_chunks, 0, u ? a.v_chunks : 0, u == 1, u == 0};
+  if (!a.latent) return {0, u ? a.v_chunks : a.k_chunks, 0, u ? a.v_chunks : 0, u == 1};
   const int mid = max(1, ((a.k_dim >> 4) + 8) >> 4), c0 = u ? mid : 0, c1 = u ? a.k_chunks : mid;
-  return {c0, c1, min(c0, a.v_tiles), min(c1, a.v_tiles), false, true};
+  return {c0, c1, min(c0, a.v_tiles), min(c1, a.v_tiles), false};
 }
 
 // ---- tokens ------------------------------------------------------------------
@@ -435,19 +461,17 @@ struct Token {
   const float *scales;
 };
 
+// e4m3 terms of q, and e5m2 terms of a probability: each of these leaves 2^-4 of what it rounds, so that
+// three give 2^-11 and four as much as the f16 that they are taken from.
 template <class T>
 struct Terms;
 template <>
 struct Terms<__nv_bfloat16> {
-  static constexpr int n = 2;
-  // Where more tiles follow they are left room; 2^-8 of the largest is still a normal e4m3, and a
-  // softmax has little of its mass below (2^-4.2 is the centre for 2048 normal scores at worst).
-  static constexpr float top = 2.f;
+  static constexpr int n = 2, p = 3;
 };
 template <>
 struct Terms<__half> {
-  static constexpr int n = 3;
-  static constexpr float top = kTop;  // (its second term would lose bits at 2^-7 of it)
+  static constexpr int n = 3, p = 4;
 };
 
 // Sums of l[0 .. N) over the warp's lanes: at each step a lane hands over half of its
@@ -477,14 +501,21 @@ struct Shape {
   static constexpr int mma = soft + gather;           // two warps that issue products: scores, values
   static constexpr int look = mma + 2;                // warps that look rows up
   static constexpr int looks = N > 32 ? 2 : 4;
-  static constexpr int tables = N > 32 ? 4 : 8;      // tiles that are looked up ahead
+  static constexpr int tables = N > 32 ? 3 : 8;      // tiles that are looked up ahead
   static constexpr int threads = 32 * (look + looks);
 };
 
 template <class T, int N>
 __global__ void __launch_bounds__(Shape<N>::threads, 1)
     attend_kernel(const AttendArgs a) {
-  constexpr int kTerms = Terms<T>::n;
+  constexpr int kTerms = Terms<T>::n, kP = Terms<T>::p;
+  // Terms of the probabilities that a token's row of 128 bytes takes; what is left (the third of 64 heads)
+  // has a tile of rows of 64 bytes behind it.
+  constexpr int kP0 = kP * N > 128 ? 128 / N : kP;
+  static_assert(kP * N <= 128 || (kP - kP0) * N == 64);
+  // Where the tensor memory has room, all terms are one product with sums of their own, which are added
+  // at the end: 44 cycles for three of 16 columns, where one after another took 120.
+  constexpr bool kMerge = kP0 == kP;
   constexpr int NC = Shape<N>::cols, kSoft = Shape<N>::soft, kGather = Shape<N>::gather, kTables = Shape<N>::tables;
   constexpr int kThreads = Shape<N>::threads;
   constexpr int kQ = kTerms * N;  // rows of Q: the terms of a head are N rows apart
@@ -627,8 +658,9 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
     for (int c = 0; c < NC; ++c) l[c] = 0.f;
     const uint32_t lanes = static_cast<uint32_t>(wl * 32) << 16;
     const int tk = wl * 32 + lane;
-    const uint32_t p_row = base + a.off_p + tk * 128;
-    bool seen = false;  // some token so far
+    const uint32_t p_row = base + a.off_p + tk * 128, p_row2 = base + a.off_p + a.tile * 128 + tk * 64;
+    bool open = true;   // some column has had no token that counts, and no offset
+    bool set = false;   // whether column c0 + gt has one
     constexpr bool kHeld = NC == 16;  // factors and offsets fit in registers
     float qf[kHeld ? NC : 1], off[kHeld ? NC : 1];
     if (kHeld) {
@@ -655,7 +687,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
           spoilt = !(meta.y < INFINITY);
           // (approximate to 2^-21, and the inverse of the very same)
           if (!spoilt) lv = lg2(fmaxf(meta.y, 0x1p-100f));
-          iv = ex2(-lv);
+          iv = ex2(-kFold - lv);
         }
       }
     };
@@ -702,7 +734,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
           most = fmaxf(most, x[c + e]);
         }
       }
-      const bool moved = soft_any<Shape<N>::groups>(grp, most > kSlack || (!seen && most > -INFINITY));
+      const bool moved = soft_any<Shape<N>::groups>(grp, most > kSlack || (open && most > -INFINITY));
       auto previous = [&] {  // O and the probabilities' buffer are free
         if (i > 0) {
           bar_wait(b_pv, (i - 1) & 1, fail);
@@ -721,20 +753,33 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
         soft_sync<Shape<N>::groups>(grp);
         if (gt < NC) {
           const int c = c0 + gt;
-          const float m = fmaxf(fmaxf(s_wmax[0][c], s_wmax[1][c]), fmaxf(s_wmax[2][c], s_wmax[3][c]));
-          const float d = m > kSlack || (!seen && m > -INFINITY) ? m - (tiles == 1 ? kTop : Terms<T>::top) : 0.f;
+          // The largest of the column goes to 2^kTop, or as far below as leaves kRoom above the largest of
+          // the warp that lies lowest: a token far above the others leaves them their bits, and
+          // is not outgrown; one among others leaves room for those that come.
+          float m = -INFINITY, low = INFINITY;
+          int warps = 0;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float x = s_wmax[w][c];
+            m = fmaxf(m, x);
+            if (x > -INFINITY) low = fminf(low, x), ++warps;
+          }
+          const float top = tiles == 1 ? kTop : warps == 1 ? kAlone : fminf(kTop, kSlack - kRoom + (m - low));
+          const bool fresh = !set && m > -INFINITY;
+          const float d = m > kSlack || fresh ? m - top : 0.f;
           s_d[c] = d;
-          s_f[c] = ex2(-d);
+          s_f[c] = fresh ? 1.f : ex2(-d);  // (the sums of one without an offset are 0)
           s_m[c] += d;
+          set |= fresh;
         }
-        soft_sync<Shape<N>::groups>(grp);
+        open = soft_any<Shape<N>::groups>(grp, gt < NC && !set);
         previous();
-        if (seen) {
+        if (i > 0) {
 #pragma unroll 1
           for (int c = 0; c < NC; c += 16) {
-            if (!__any_sync(0xffffffffu, s_d[c0 + c + (lane & 15)] != 0.f)) continue;
+            if (!__any_sync(0xffffffffu, s_f[c0 + c + (lane & 15)] != 1.f)) continue;
 #pragma unroll 1
-            for (int j = 0; j < a.v_tiles; ++j) {
+            for (int j = 0; j < a.v_tiles * a.sums; ++j) {
               uint32_t o[16];
               const uint32_t at = t_o + lanes + j * N + c0 + c;
               tc_ld16(at, o);
@@ -754,7 +799,6 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
           x[c] -= d;
           if (kHeld) off[kHeld ? c : 0] += d;
         }
-        seen = true;
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -766,23 +810,27 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       if (!moved) previous();
       if (tk < ((cn + 31) & ~31)) {
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t)
+        for (int c = 0; c < NC; c += 16) {
+          uint32_t w[kP][4];
 #pragma unroll
-          for (int c = 0; c < NC; c += 16) {
-            uint32_t w[4];
+          for (int e = 0; e < 4; ++e) {
+            float *y = x + c + 4 * e;
+            // (in f16 behind the first term; for bf16, whose terms end above it, from the start)
+            if (kP > 3) w[0][e] = take_e5m2(y[0], y[1]) | take_e5m2(y[2], y[3]) << 16;
+            __half2 g = __floats2half2_rn(y[0], y[1]), h = __floats2half2_rn(y[2], y[3]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float *y = x + c + 4 * e;
-              if (t + 1 < kTerms) {
-                w[e] = take_term<false>(y[0], y[1]);
-                w[e] |= take_term<false>(y[2], y[3]) << 16;
-              } else {
-                w[e] = take_term<true>(y[0], y[1]);
-                w[e] |= take_term<true>(y[2], y[3]) << 16;
-              }
+            for (int t = kP > 3 ? 1 : 0; t < kP; ++t) {
+              w[t][e] = take_e5m2(g);
+              w[t][e] |= take_e5m2(h) << 16;
             }
-            st_shared4(p_row + (((t * N + c0 + c) >> 4 ^ (tk & 7)) << 4), w[0], w[1], w[2], w[3]);
           }
+#pragma unroll
+          for (int t = 0; t < kP; ++t) {
+            const int at = t * N + c0 + c;
+            st_shared4(t < kP0 ? p_row + ((at >> 4 ^ (tk & 7)) << 4) : p_row2 + (((at - kP0 * N) >> 4 ^ (tk >> 1 & 3)) << 4),
+                       w[t][0], w[t][1], w[t][2], w[t][3]);
+          }
+        }
       }
       fence_async();
       tc_before();
@@ -800,8 +848,8 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       const int c = c0 + gt;
       const float z = (s_wmax[0][c] + s_wmax[1][c]) + (s_wmax[2][c] + s_wmax[3][c]);
       s_l[c] = z;
-      if (!seen) s_m[c] = kNone;
-      s_f[c] = z > 0.f || z != z ? 1.f / z : 0.f;
+      if (!set) s_m[c] = kNone;
+      s_f[c] = z > 0.f || z != z ? exp2f(-kFold) / z : 0.f;
     }
     if (tiles > 0) {
       bar_wait(b_pv, (tiles - 1) & 1, fail);
@@ -928,7 +976,12 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       const Token now = token(x.r, t0 + nt * a.tile + j);
       fetch(x, at, as);
       advance(at, as);
-      if (ns == 0 && nt >= kTables) bar_wait(b_used + 8 * slot, (nt / kTables - 1) & 1, fail);
+      bool put = n >= kAhead;  // the scales of the step before the last
+      if (ns == 0 && nt >= kTables) {
+        if (put) put_scales(x, bt, bs), advance(bt, bs);
+        put = false;
+        bar_wait(b_used + 8 * slot, (nt / kTables - 1) & 1, fail);
+      }
       if (j < a.tile) {
         const uint32_t to = base + a.off_rows + (slot * a.tile + j) * 8;
         asm volatile("st.shared.b64 [%0], %1;" ::"r"(to), "l"(now.row ? now.row + k_at : zeros) : "memory");
@@ -938,10 +991,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       }
       if (ns == per - 1) bar_arrive(b_tab + 8 * slot);
       advance(nt, ns);
-      if (n >= kAhead) {
-        put_scales(x, bt, bs);
-        advance(bt, bs);
-      }
+      if (put) put_scales(x, bt, bs), advance(bt, bs);
       const int32_t *sc = reinterpret_cast<const int32_t *>(now.scales);
       x.use = now.row != 0;
       x.k = ld_if(sc, x.use, 0);
@@ -964,7 +1014,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
   } else {
     // ---- products: a warp for the scores and one for the values; one lane issues -----------
     const uint32_t d_qk = mma_desc(kQ, false, false);
-    const uint32_t d_pv = mma_desc(N, false, true), d_pv5 = mma_desc(N, true, true);
+    const uint32_t d_pv = mma_desc(N, true, true), d_pvs = mma_desc(kP * N, true, true);
     const int k_steps = (a.k_dim + 31) >> 5;
     const bool elected = elect_one();
     const uint32_t q_desc = smem_desc(base + a.off_q), p_desc = smem_desc(base + a.off_p);
@@ -996,13 +1046,20 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       uint32_t v = smem_desc(base + s * a.stage_bytes) + ((half.is_v ? a.k_chunks : 0) + half.v0) * a.tile * 8;
       if (elected) {
         for (int j = half.v0; j < half.v1; ++j, v += a.tile * 8) {
-          const uint32_t d = t_o + j * N;
-          uint32_t p = p_desc, w = v;
+          const uint32_t d = t_o + j * a.sums * N;
+          if (kMerge && a.sums > 1) {
+            uint32_t p = p_desc, w = v;
 #pragma unroll 2
-          for (int k = 0; k < steps; ++k, p += 256, w += 256)
+            for (int k = 0; k < steps; ++k, p += 256, w += 256) mma_f8(d, w, p, d_pvs, i > 0 || k > 0);
+            continue;
+          }
+          uint32_t p = p_desc, p2 = p_desc + a.tile * 8, w = v;
+#pragma unroll 2
+          for (int k = 0; k < steps; ++k, p += 256, p2 += 128, w += 256) {
 #pragma unroll
-            for (int t = 0; t < kTerms; ++t)
-              mma_f8(d, w, p + t * N / 16, t + 1 < kTerms ? d_pv : d_pv5, t > 0 ? 1 : i > 0 || k > 0);
+            for (int t = 0; t < kP0; ++t) mma_f8(d, w, p + t * N / 16, d_pv, t > 0 ? 1 : i > 0 || k > 0);
+            if (kP0 < kP) mma_f8<kDescHi64>(d, w, p2, d_pv, 1);
+          }
         }
         if (half.v0 < half.v1) tc_commit(b_empty + 16 * s + 8 * u);
         if (u == 1) {
@@ -1091,8 +1148,22 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
         const int d = j * 128 + wl * 32 + lane;
         uint32_t o[16];
         if (tiles > 0) {
-          tc_ld16(t_o + lanes + j * N + c, o);
-          tc_wait_ld16(o);
+          const uint32_t at = t_o + lanes + j * a.sums * N + c;
+          tc_ld16(at, o);
+          if (kMerge && a.sums > 1) {
+            uint32_t y[kP - 1][16];
+#pragma unroll
+            for (int t = 1; t < kP; ++t) tc_ld16(at + t * N, y[t - 1]);
+            tc_wait_ld16(o);
+#pragma unroll
+            for (int t = 1; t < kP; ++t) {
+              tc_wait_ld16(y[t - 1]);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(y[t - 1][e]));
+            }
+          } else {
+            tc_wait_ld16(o);
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = 0;
@@ -1146,7 +1217,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
       }
       s_m[tid] = m;
       s_l[tid] = z;
-      s_f[tid] = z > 0.f || z != z ? 1.f / z : 0.f;
+      s_f[tid] = z > 0.f || z != z ? exp2f(-kFold) / z : 0.f;
     }
     __syncthreads();
   }
@@ -1154,7 +1225,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
   if (a.lse && tid < mine) {
     const float z = s_l[tid];
     a.lse[qrow * a.heads + h0 + first + tid] =
-        z > 0.f || z != z ? (s_m[tid] + log2f(z)) * 0.6931471805599453f : -INFINITY;
+        z > 0.f || z != z ? (s_m[tid] + (kFold + log2f(z))) * 0.6931471805599453f : -INFINITY;
   }
   if (lone) {
     const uint32_t total = heads * (a.quads.d >> 1);
@@ -1202,7 +1273,7 @@ constexpr uint32_t kSmemSm = 233472;     // of an SM; a CTA takes its own and 1 
 constexpr uint32_t kSmemCta = 232448;    // at most, static and dynamic
 
 // Tile, stages and offsets for N heads; false where they do not fit in `limit` bytes.
-bool plan_smem(AttendArgs &a, int N, int terms, int tables, int tile, uint32_t limit, uint32_t &bytes) {
+bool plan_smem(AttendArgs &a, int N, int terms, int p_terms, int tables, int tile, uint32_t limit, uint32_t &bytes) {
   a.tile = tile;
   a.k_chunks = (a.k_dim + 127) / 128;
   a.v_tiles = (a.v_dim + 127) / 128;
@@ -1210,7 +1281,7 @@ bool plan_smem(AttendArgs &a, int N, int terms, int tables, int tile, uint32_t l
   // (a latent record whose V is wider than its K's chunks cannot be: v_dim <= k_dim)
   a.stage_bytes = static_cast<uint32_t>(a.k_chunks + a.v_chunks) * tile * 128;
   const uint32_t q = static_cast<uint32_t>(terms) * a.k_chunks * N * 128;
-  const uint32_t p = tile * 128;
+  const uint32_t p = tile * (p_terms * N > 128 ? 192 : 128);
   // rows beyond a tile that the 128-row products read stay inside: Q and P follow
   const uint32_t over = (128 - tile) * 128;
   const uint32_t rest = q + p + (q + p < over ? over - q - p : 0);
@@ -1284,10 +1355,12 @@ int plan_attend(const AttendArgs &args, int64_t pairs, Plan &best) {
   a.hgroups = (a.group + N - 1) / N;
   const int64_t units = pairs * a.hgroups;
   constexpr int kTerms = Terms<T>::n;
-  // TMEM: two score buffers and the sums, a power of two of columns.
+  // TMEM: two score buffers and the sums, those of each term where there is room, a power of two of columns.
+  constexpr int kP = Terms<T>::p;
   int cols = 32;
   a.v_tiles = (a.v_dim + 127) / 128;
-  while (cols < 2 * kTerms * N + a.v_tiles * N) cols *= 2;
+  a.sums = kP * N <= 128 && 2 * kTerms * N + a.v_tiles * kP * N <= 512 ? kP : 1;
+  while (cols < 2 * kTerms * N + a.v_tiles * a.sums * N) cols *= 2;
   a.tmem_cols = cols;
   const int64_t tokens = static_cast<int64_t>(a.entries) * a.rec_tokens.d;
   auto fn = attend_kernel<T, N>;
@@ -1311,12 +1384,12 @@ int plan_attend(const AttendArgs &args, int64_t pairs, Plan &best) {
   const uint32_t least = std::min(whole, kSmemSm / 512 * cols - 1024);
   uint32_t bytes = 0;
   bool ok = false;
-  for (int tile = 128; tile >= 64 && !ok; tile -= 32) ok = plan_smem(a, N, kTerms, Shape<N>::tables, tile, whole, bytes);
+  for (int tile = 128; tile >= 64 && !ok; tile -= 32) ok = plan_smem(a, N, kTerms, Terms<T>::p, Shape<N>::tables, tile, whole, bytes);
   if (!ok) return HISPARSE_OK;  // the widest rows leave no room for two tiles of so many heads
   bytes = std::max(bytes, least);
   const double copy = 400 + a.tile * (a.k_dim + (a.latent ? 0 : a.v_dim)) / 27.0;
   const double products = (a.k_dim + 31) / 32 * std::max(40.0, 32 + kTerms * N / 4.0) +
-                          a.v_tiles * (a.tile / 32) * kTerms * std::max(40.0, 32 + N / 4.0);
+                          a.v_tiles * (a.tile / 32) * (a.sums > 1 ? std::max(40.0, 32 + kP * N / 4.0) : kP * std::max(40.0, 32 + N / 4.0));
   const double turn = std::max({copy, products, N > 32 ? 2000.0 : 1200.0, 7400.0 / a.stages});
   for (int c = 1; c <= kMaxCluster; c *= 2) {
     if (c > 1 && tokens < 64 * c) break;

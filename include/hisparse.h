@@ -624,9 +624,11 @@ typedef struct {
  *   s_j = softmax_scale * q . (k_j * sK),  out = sum_j softmax(s)_j (v_j * sV),
  * lse = log sum_j exp(s_j).  A row with nothing to read gives out 0 and lse
  * -inf.  Scores, softmax and sums are in 32 bits; K and V enter the tensor
- * cores as the e4m3 they are, q and the probabilities as sums of 8-bit terms, two for
- * bf16 and three for f16: q at least as fine as its type, a probability p within
- * max(2^-8 p, 2^-16 of the row's largest) (f16: 2^-13, 2^-20).  A scale of V below 2^-100 counts as 2^-100.
+ * cores as the e4m3 they are, q and the products p * sV of a probability and its scale of V as sums of
+ * 8-bit terms.  q is exact down to 2^-9 (f16: 2^-6) of the head's largest value, and within 2^-17 of that
+ * below.  p * sV is within 2^-11 (f16: 2^-15) of itself, or, if that is more, within 2^-32 of the largest
+ * where a token stands out (by 2^12 from those beside it), and at worst within 2^-20 of it.
+ * A scale of V below 2^-100 counts as 2^-100.
  * A NaN scale of K gives NaN in out and lse of the rows that read it; one of V that is NaN or
  * infinite in out alone.  A slot
  * outside what B, resident and -1 allow, or a selected position outside

@@ -7,8 +7,8 @@ import torch
 
 from host_offload_serving_gb300 import cache8, pages
 from host_offload_serving_gb300 import hisparse as H
-from test_cache8_gpu import (E4M3, HEADS, LATENT, PageModel, _attend, _attend64, _attend_case, _attend_close, _gen,
-                             _pack64, _pack_close, _randn, _rotated64, _same, _status)
+from test_cache8_gpu import (E4M3, HEADS, LATENT, U, PageModel, _attend, _attend64, _attend_case, _attend_close,
+                             _gen, _pack64, _pack_close, _randn, _rotated64, _same, _status)
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +170,48 @@ def test_attend_infinite_scales_of_k():
     assert bool((~torch.isfinite(c["out"][~low])).all()) and bool((~torch.isfinite(c["lse"][~low])).all())
     m = low.cpu().numpy()
     _attend_close(c["out"][low][None, None], c["lse"][low][None, None], [x[m][None, None] for x in want], torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rec,heads,R,at", [
+    (LATENT, 128, 1, 0), (LATENT, 128, 80, 5), (LATENT, 16, 160, 2040), (LATENT, 64, 2, 700),
+    (HEADS, 16, 40, 0), (HEADS, 16, 1, 1300), (HEADS, 128, 1, 0), (cache8.Records(2, 64, 64, 32), 6, 160, 1),
+])
+@pytest.mark.parametrize("weight", [0.5, 0.95, 0.997, 0.9999])
+def test_attend_beside_a_dominant_token_without_values(rec, heads, R, at, weight, dtype):
+    """One token has most of the weight and a V of 0, so that the output is made of the others'
+    small probabilities.  Its error is bounded by itself: the rounding of the output (at most
+    U / 3^0.5 of its norm, 2^-25 a value at the lower end of f16) with half as much again, 2^-11 of each
+    probability, and 2^-32 of the largest probability times its scale of V (half as much again over
+    3^0.5), by the norm of V's bytes."""
+    n, D, K = 2048, rec.k_dim, rec.kv_heads
+    c = _attend_case(rec, heads, dtype, R, 1, n, pad=0.0)
+    hot, scales = c["hot"].view(E4M3), c["scales"]
+    far = torch.arange(K, device="cuda") * D + D - 1
+    hot[..., far] = torch.tensor(0.0, device="cuda").to(E4M3)
+    c["q"][..., D - 1] = 1.0
+    slot = c["slots"][:, at].long()
+    hot[torch.arange(R, device="cuda"), slot] = torch.tensor(0.0, device="cuda").to(E4M3)
+    for f in far.tolist():
+        hot[torch.arange(R, device="cuda"), slot, f] = torch.tensor(448.0, device="cuda").to(E4M3)
+    # a block of its own, whose scale makes its score what the weight asks for
+    blk = scales.shape[1]
+    c["sel"][:, at] = blk * rec.block_tokens
+    c["scales"] = torch.cat([scales, torch.full((R, 1, rec.columns), 1 / 60, device="cuda")], 1).contiguous()
+    some = [0, R - 1] if R > 1 else [0]
+    pick = lambda: _attend64(rec, c["q"][some], c["sel"][some], c["slots"][some], c["hot"][some], c["scales"][some], D ** -0.5)
+    c["scales"][:, blk, :K] = -50.0
+    rest = float(np.median(pick()[1]))                    # lse of the others
+    c["scales"][:, blk, :K] = (rest + np.log(weight / (1 - weight))) * D ** 0.5 / 448
+    assert _attend(c) == 0
+    want, lse, _, _ = pick()
+    got = c["out"][some].double().cpu().numpy()
+    size = np.linalg.norm(want, axis=-1)
+    err = np.linalg.norm(got - want, axis=-1) / size
+    v_cols = rec.v_dim if rec.latent else K * rec.v_dim
+    bytes_v = hot[some][..., :v_cols] if rec.latent else hot[some][..., K * D:]
+    norm_v = float(bytes_v.double().norm(dim=(1, 2)).max()) / (1 if rec.latent else K ** 0.5)
+    s_v = float(c["scales"][:, blk, 0 if rec.latent else K].max())
+    low = 0.0 if dtype is torch.bfloat16 else 2.0 ** -25 * rec.v_dim ** 0.5 / size
+    tol = 1.5 * (U[dtype] + low) / 3 ** 0.5 + 2.0 ** -11 + 1.5 * 2.0 ** -32 / 3 ** 0.5 * weight * s_v * norm_v / size
+    assert (err <= tol).all(), (float((err / tol).max()), float(err.max()), float(tol.min()))
