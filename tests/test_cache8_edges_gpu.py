@@ -215,3 +215,30 @@ def test_attend_beside_a_dominant_token_without_values(rec, heads, R, at, weight
     low = 0.0 if dtype is torch.bfloat16 else 2.0 ** -25 * rec.v_dim ** 0.5 / size
     tol = 1.5 * (U[dtype] + low) / 3 ** 0.5 + 2.0 ** -11 + 1.5 * 2.0 ** -32 / 3 ** 0.5 * weight * s_v * norm_v / size
     assert (err <= tol).all(), (float((err / tol).max()), float(err.max()), float(tol.min()))
+
+
+@pytest.mark.parametrize("rec,heads", [(HEADS, 16), (cache8.Records(1, 128, 128, 16), 64)])
+def test_attend_first_tile_of_scores_of_minus_infinity(rec, heads):
+    """A head whose first tile has only a score of minus infinity takes its offset from later tiles
+    (other heads of the tile have one of plus infinity, and no result)."""
+    c = _attend_case(rec, heads, torch.bfloat16, 1, 1, 4096, pad=0.0)
+    K, D = rec.kv_heads, rec.k_dim
+    hot = c["hot"].view(E4M3)
+    far = torch.arange(K, device="cuda") * D + D - 1      # the last value of each K head
+    hot[..., far] = torch.tensor(-448.0, device="cuda").to(E4M3)
+    c["scales"][..., :K] = 1 / 64
+    c["q"][..., D - 1] = 300.0 * D ** 0.5 / 7.0           # scores of about -300
+    c["q"][:, :, 1::2, D - 1] *= -1.0                     # and of 300
+    c["scales"] = torch.cat([c["scales"], torch.ones(1, 1, rec.columns, device="cuda")], 1).contiguous()
+    c["scales"][0, -1, :K] = float("inf")
+    c["sel"][0, :128] = c["slots"][0, :128] = -1
+    c["slots"][0, 128:][c["slots"][0, 128:] == 0] = -1
+    hot[0, 0, :K * D] = torch.tensor(0.0, device="cuda").to(E4M3)
+    hot[0, 0, far] = torch.tensor(-448.0, device="cuda").to(E4M3)
+    gone = c["slots"].clone()
+    c["slots"][0, 77], c["sel"][0, 77] = 0, (c["scales"].shape[1] - 1) * rec.block_tokens
+    assert _attend(c) == 0
+    want = _attend64(rec, c["q"], c["sel"], gone, c["hot"], c["scales"], D ** -0.5)
+    even = [x[:, :, ::2] for x in want]
+    _attend_close(c["out"][:, :, ::2], c["lse"][:, :, ::2], even, torch.bfloat16)
+    assert bool(torch.isnan(c["out"][:, :, 1::2]).all())
