@@ -446,7 +446,8 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) pack_kernel(const Pack
         s = fmaxf(m * ((has_last ? 1.f : a.headroom) / 448.f), 0x1p-100f);
         if (tid == 0 && mine) *scale_p = s;
       }
-      inv = s > 0.f ? 1.f / s : 0.f;
+      // (without a scale all finite values are 0, and the others stay what they are)
+      inv = s > 0.f ? 1.f / s : s == 0.f ? 1.f : 0.f;
     }
     if (step < chunks && chunks > 1) continue;
 #pragma unroll

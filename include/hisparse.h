@@ -576,9 +576,8 @@ typedef struct {
  *   call also holds the block's last position (amax 0 leaves it 0, not set);
  * - else the block is open and its scale stands.
  * A value x is stored as e4m3(x * (1 / scale)), rounded to nearest even, saturating
- * at 448; infinities do not count in amax and saturate; NaN stays NaN.  A scale is at least
- * 2^-100.  A decode step's
- * rows are d_new_rows of hisparse_resolve_step; a prompt's go to the host pool,
+ * at 448; infinities do not count in amax and saturate, also where no scale is set; NaN stays NaN.  A
+ * scale is at least 2^-100.  A decode step's rows are d_new_rows of hisparse_resolve_step; a prompt's go to the host pool,
  * a mirror or the resident store.  Start the scales of a new request at 0.
  * A position outside [0, scale_blocks * block_tokens), a request outside
  * [0, R), a sequence that passes position 2^31 - 1, or a row outside dst sets

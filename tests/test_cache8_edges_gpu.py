@@ -46,6 +46,23 @@ def test_pack_blocks_walked_by_teams_with_threads_left_over(rec, rot):
     _pack_close(torch.cat([dst[i, start[i]:start[i] + lens[i]] for i in range(2)]), want)
 
 
+@pytest.mark.parametrize("rec", [LATENT, HEADS, cache8.Records(2, 80, 48, 1)], ids=["latent", "heads", "one"])
+def test_pack_blocks_whose_only_values_are_infinite(rec):
+    """Infinities saturate also where nothing else sets a scale; it stays unset."""
+    k = torch.zeros(3, rec.kv_heads, rec.k_dim, device="cuda")
+    k[0, 0, 3], k[1, 0, 5], k[2, 0, 7] = float("inf"), float("-inf"), float("nan")
+    v = None if rec.latent else torch.zeros(3, rec.kv_heads, rec.v_dim, device="cuda")
+    scales = torch.zeros(1, rec.blocks(3), rec.columns, device="cuda")
+    rows = torch.full((3, rec.row_bytes), 0x55, dtype=torch.uint8, device="cuda")
+    cache8.pack(rec, k, v, rows, scales, _i32([0]), max_len=3)
+    want = torch.zeros_like(rows)
+    want[0, 3], want[1, 5], want[2, 7] = 0x7E, 0xFE, 0x7F
+    got = rows.clone()
+    got[2, 7] &= 0x7F
+    assert torch.equal(got, want)
+    assert bool((scales == 0).all())
+
+
 # ---------------------------------------------------------------------------------------------
 # where tensors lie
 # ---------------------------------------------------------------------------------------------
