@@ -23,7 +23,7 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 
 // d_work: word 0 the number of copies, word 1 the pages in use; then three arrays of `span`
 // = max(num_pages, num_requests) words: the pages copied from, the pages copied to,
-// and the rows of each copy (fork) or where each page moved (compact).  With
+// and the rows of each copy (fork) or which move is each page's (compact).  With
 // grow and fork the third array first holds the list's demands, and the second the free
 // pages by rank.
 constexpr int kWorkHead = 16;
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PoolAr
   const int movers = m - low;
   for (int j = rank * kPlanThreads + threadIdx.x; j < movers; j += kPlanCtas * kPlanThreads) {
     const int f = from[j], t = to[j];
-    moved[f] = t;
+    moved[f] = j;
     a.refs[t] = a.refs[f];
     a.refs[f] = 0;
   }
@@ -455,11 +455,13 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const PoolArgs 
     for (int64_t e = tid; e < static_cast<int64_t>(a.R) * a.blocks; e += step) {
       const int p = a.tables[e];
       if (p < m) continue;
-      const int t = p < a.pages ? third[p] : -1;
-      if (t >= 0 && t < m) {
-        a.tables[e] = t;
+      // Its move, if the list of moves says so too: a page that no count stands for has none, and an
+      // earlier call's word in the place of it.
+      const int j = p < a.pages ? third[p] : -1;
+      if (j >= 0 && j < copies && from[j] == p) {
+        a.tables[e] = to[j];
       } else {
-        report(a, HISPARSE_ERR_RANGE);  // an entry that no count stands for
+        report(a, HISPARSE_ERR_RANGE);
       }
     }
   }

@@ -690,7 +690,8 @@ int hisparse_pages_free(const hisparse_page_pool *p, const int32_t *d_reqs, int3
 
 /* Move the pages in use to the front of the store: with m pages in use, the
  * j-th of those at or above m moves to the j-th free page below m, in every
- * layer, and every table follows.  No other page moves.  Errors: EINVAL, EBOUND, ECUDA. */
+ * layer, and every table follows.  No other page moves.  A table entry at or above m whose page no count
+ * stands for stays as it is, with HISPARSE_ERR_RANGE.  Errors: EINVAL, EBOUND, ECUDA. */
 int hisparse_pages_compact(const hisparse_page_pool *p, void *stream);
 
 /* (Library calls.)

@@ -123,6 +123,27 @@ def test_pages_grow_by_more_than_31_bits():
     assert int((pool.tables != -1).sum()) == 15
 
 
+def test_pages_compact_reports_entries_that_no_count_stands_for():
+    """A table entry whose page has no count is reported and stays, whatever an earlier call left in
+    the workspace."""
+    model = PageModel(64, 4, 8, 4, 1, 16, 3)
+    st = _status()
+    pool = pages.PagePool(torch.from_numpy(model.store.copy()).cuda(), block_tokens=4, requests=4, max_blocks=8,
+                          status=st)
+    pool.grow(_i32([0, 1]), _i32([3, 4]))
+    model.grow([0, 1], [3, 4])
+    pool.free(_i32([0]))
+    model.free([0])
+    pool.tables[2, 5] = 40
+    model.tables[2, 5] = 40
+    pool.work.fill_(1)
+    pool.compact()
+    model.compact()
+    assert int(st) == H.ERR_RANGE
+    st.zero_()
+    _same(pool, model, st)
+
+
 # ---------------------------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------------------------
