@@ -43,28 +43,49 @@ __device__ __forceinline__ void report(const PoolArgs &a, uint32_t bit) {
 }
 
 // Sum over the CTA and this thread's exclusive prefix; all threads call it.
-template <class T>
-__device__ __forceinline__ T block_scan(T v, T *warp_sums, T &total) {
+__device__ __forceinline__ int block_scan(int v, int *warp_sums, int &total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  T x = v;
+  int x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();
   if (lane == 31) warp_sums[w] = x;
   __syncthreads();
-  const T s = warp_sums[lane];  // kPlanWarps == 32
-  T t = s;
+  const int s = warp_sums[lane];  // kPlanWarps == 32
+  int t = s;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, t, o);
+    const int y = __shfl_up_sync(0xffffffffu, t, o);
     if (lane >= o) t += y;
   }
   total = __shfl_sync(0xffffffffu, t, 31);
-  const T before = __shfl_sync(0xffffffffu, t - s, w);
+  const int before = __shfl_sync(0xffffffffu, t - s, w);
   return before + x - v;
+}
+// The same of values up to `most` (at most 2^30 + 1) whose sums stay at it once they reach it.
+__device__ __forceinline__ uint32_t block_scan_to(uint32_t v, uint32_t most, int *warp_sums, uint32_t &total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x = min(x + y, most);
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[w] = x;
+  __syncthreads();
+  uint32_t t = warp_sums[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) t = min(t + y, most);
+  }
+  total = __shfl_sync(0xffffffffu, t, 31);
+  const uint32_t before = __shfl_sync(0xffffffffu, t, max(w - 1, 0)), left = __shfl_up_sync(0xffffffffu, x, 1);
+  return min((w > 0 ? before : 0) + (lane > 0 ? left : 0), most);
 }
 
 // Every CTA of the cluster learns the totals of all CTAs: `tell`, a cluster barrier, `learn`, which
@@ -278,7 +299,6 @@ __device__ void grow_entry(const PoolArgs &a, int i, int part, int parts, int r,
 template <bool kFork>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
   __shared__ int warp_sums[32], slot[kPlanCtas], s_part[kPlanWarps];
-  __shared__ long long wide_sums[32];
   pdl_wait();
   pdl_launch();
   cg::cluster_group cluster = cg::this_cluster();
@@ -318,21 +338,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PoolArgs a) {
   cluster.barrier_wait();
   tell(total, slot);
   cluster.sync();
-  // every CTA ranks the whole list: thread t takes a run of entries (in 64 bits: a list may ask for
-  // more than 2^31 pages, and its first entries still get theirs)
+  // every CTA ranks the whole list: thread t takes a run of entries.  (The list may ask for more than
+  // 2^31 pages, and its first entries still get theirs: one more than there are pages is all that counts.)
   const int run = (a.n + kPlanThreads - 1) / kPlanThreads;
   const int i0 = min(a.n, static_cast<int>(threadIdx.x) * run), i1 = min(a.n, i0 + run);
-  long long mine = 0, demand;
-  for (int i = i0; i < i1; ++i) mine += max(0, third[i]);
-  long long at = block_scan(mine, wide_sums, demand);
+  const uint32_t most = a.pages + 1u;
+  uint32_t mine = 0, demand;
+  for (int i = i0; i < i1; ++i) mine = min(mine + min(static_cast<uint32_t>(max(0, third[i])), most), most);
+  uint32_t at = block_scan_to(mine, most, warp_sums, demand);
   int free_pages;
   const int before = learn(slot, free_pages);
-  list_free(a, slice, words, bits, before, static_cast<int>(min(demand, static_cast<long long>(a.pages))), to, warp_sums);
+  list_free(a, slice, words, bits, before, static_cast<int>(min(demand, most - 1)), to, warp_sums);
   // the demands that fit are a prefix of the list; `from` keeps each entry's first rank
   for (int i = i0; i < i1; ++i) {
-    const int need = max(0, third[i]);
-    if (rank == 0) from[i] = need > 0 && at + need > free_pages ? -1 : static_cast<int>(min(at, static_cast<long long>(INT_MAX)));
-    at += need;
+    const uint32_t need = min(static_cast<uint32_t>(max(0, third[i])), most);
+    if (rank == 0) from[i] = need > 0 && at + need > static_cast<uint32_t>(free_pages) ? -1 : static_cast<int>(at);
+    at = min(at + need, most);
   }
   cluster.sync();  // the free list, the ranks; everyone has read every demand
   if (kFork) {
