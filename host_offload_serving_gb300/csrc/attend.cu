@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
           k.row = base0 + static_cast<uint64_t>(is_near ? near : far) * (is_near ? a.hot_row : a.res_row);
           if (!plain) k.row += static_cast<uint64_t>(sub) * a.row_bytes;
           k.scales = scales + blk * a.columns;
-        } else if (a.status && !(inside && pos >= seq)) {
+        } else if (a.status && !(pos < 0x80000000u && pos >= seq)) {  // (beyond seq the table may end)
           atomicOr(a.status, HISPARSE_ERR_RANGE);
         }
       }

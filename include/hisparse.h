@@ -631,7 +631,8 @@ typedef struct {
  * A NaN scale of K gives NaN in out and lse of the rows that read it; one of V that is NaN or
  * infinite in out alone.  A slot
  * outside what B, resident and -1 allow, or a selected position outside
- * the scale table or of 2^31 or more, sets HISPARSE_ERR_RANGE and is left out.
+ * the scale table or of 2^31 or more, sets HISPARSE_ERR_RANGE and is left out; a position at or beyond
+ * d_seq_lens does not count and needs neither.
  * HISPARSE_ERR_WAIT: a wait inside the kernel ran out (it ends, with NaN in out and lse of the rows
  * concerned, whether or not there is a d_status).
  * Results do not depend on timing.  q, out, hot and resident are 16-byte aligned.

@@ -280,3 +280,19 @@ def test_attend_first_tile_of_scores_of_minus_infinity(rec, heads):
     even = [x[:, :, ::2] for x in want]
     _attend_close(c["out"][:, :, ::2], c["lse"][:, :, ::2], even, torch.bfloat16)
     assert bool(torch.isnan(c["out"][:, :, 1::2]).all())
+
+
+@pytest.mark.parametrize("seq,tok,block", [(100, 16, 1), (1000, 64, 16), (7, 5, 2)])
+def test_attend_last_page_beyond_the_scale_table(seq, tok, block):
+    """Tokens of a part-filled last page do not count, whether or not the scale table reaches them."""
+    rec = cache8.Records(2, 64, 64, block)
+    n = -(-seq // tok)
+    c = _attend_case(rec, 8, torch.bfloat16, 2, 1, n, tok=tok, pad=0.0)
+    c["sel"] = torch.stack([torch.randperm(n, device="cuda") for _ in range(2)]).int()
+    c["scales"] = c["scales"][:, :rec.blocks(seq)].contiguous()
+    lens = _i32([seq, seq])
+    assert rec.blocks(seq) * block < n * tok
+    assert _attend(c, record_tokens=tok, seq_lens=lens) == 0
+    want = _attend64(rec, c["q"], c["sel"], c["slots"], c["hot"], c["scales"], 64 ** -0.5, tok=tok, seq_lens=lens)
+    _attend_close(c["out"], c["lse"], want, torch.bfloat16)
+    assert _attend(c, record_tokens=tok) == H.ERR_RANGE      # without lengths they are selected
