@@ -151,7 +151,11 @@ __device__ __forceinline__ float2 rotary_cos_sin(int32_t position, int64_t turns
   const int64_t phase = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(position)) *
                                              static_cast<uint64_t>(turns));
   float s, c;
-  // (half turns in [-1, 1); the 32 bits left out are below 2^-31 of one, 32-bit results are not as fine)
-  sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &s, &c);
+  // Half turns in [-1, 1], rounded to 32 bits from all 64: the sine of an angle far below a turn (slow
+  // pairs, small positions) is as fine as any.  By two conversions of 32 bits, as one of 64 is slow.
+  const uint64_t mag = phase < 0 ? 0 - static_cast<uint64_t>(phase) : static_cast<uint64_t>(phase);
+  const float half_turns = fmaf(__uint2float_rn(static_cast<uint32_t>(mag)), 0x1p-63f,
+                                __uint2float_rn(static_cast<uint32_t>(mag >> 32)) * 0x1p-31f);
+  sincospif(phase < 0 ? -half_turns : half_turns, &s, &c);
   return make_float2(c * amplitude, s * amplitude * sign);
 }

@@ -18,6 +18,27 @@ def _i32(x):
 
 
 # ---------------------------------------------------------------------------------------------
+# rotary
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotary_sines_of_small_angles(interleaved):
+    """The sine of an angle far below a turn is as fine, relatively, as its 32 bits."""
+    rot, T = 64, 6
+    turns, _ = cache8.rotary_turns(rot, base=1e9)
+    pos = _i32([1, 3, 100, -1, -7, 4097])
+    x = torch.zeros(T, 1, rot, device="cuda")
+    even = torch.arange(0, rot, 2) if interleaved else torch.arange(rot // 2)
+    x[..., even + (1 if interleaved else rot // 2)] = 1.0    # pairs (0, 1) -> (-sin, cos)
+    y = cache8.rotate(x, pos, turns.cuda(), interleaved=interleaved, out=torch.empty_like(x))[0]
+    want, _ = _rotated64(x, pos, turns, 0, interleaved, 1.0)
+    got, want = y.double().cpu().numpy()[..., even], want[..., even]
+    # the phase rounded to 24 bits, sincospif (2 units in the last place), one product
+    rel = np.abs(got - want) / np.abs(want)
+    small = np.abs(want) < 0.25
+    assert small.sum() > 50 and rel[small].max() <= 4 * 2.0 ** -23
+
+
+# ---------------------------------------------------------------------------------------------
 # pack
 # ---------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("rec,rot", [
