@@ -44,20 +44,21 @@ def build(force=False, verbose=False):
     if verbose:
         flags.insert(0, "-Xptxas=-v")
 
-    def compile_one(src):
-        obj = os.path.join(PKG, "_build", os.path.basename(src) + tag + ".o")
+    objs = [os.path.join(os.path.dirname(OUT), os.path.basename(src) + tag + ".o") for src in SRCS]
+
+    def compile_one(src, obj):
         cmd = [exe, *flags, "-c", "-o", obj, src]
         if verbose:
             print(" ".join(cmd))
         subprocess.check_call(cmd)
-        return obj
 
-    with ThreadPoolExecutor(len(SRCS)) as ex:
-        objs = list(ex.map(compile_one, SRCS))
     try:
+        with ThreadPoolExecutor(len(SRCS)) as ex:
+            list(ex.map(compile_one, SRCS, objs))
         subprocess.check_call([exe, *ARCH, "-shared", "-o", OUT + tag, *objs])
         os.replace(OUT + tag, OUT)
     finally:
-        for o in objs:
-            os.remove(o)
+        for path in (*objs, OUT + tag):
+            if os.path.exists(path):
+                os.remove(path)
     return OUT

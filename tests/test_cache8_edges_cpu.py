@@ -1,8 +1,11 @@
 """What the 8-bit record operators refuse before a launch, beyond test_cache8_cpu.py."""
+import os
+import subprocess
+
 import pytest
 import torch
 
-from host_offload_serving_gb300 import cache8, pages
+from host_offload_serving_gb300 import _build, cache8, pages
 from host_offload_serving_gb300 import hisparse as H
 
 REC = cache8.Records(2, 64, 64, 16)
@@ -49,3 +52,22 @@ def test_pages_bound_on_blocks():
     assert H.hisparse_pages_fork(p, 0x1000, 0x1000, 0x1000, 1, None) == H.EBOUND
     assert H.hisparse_pages_free(p, 0x1000, 1, None) == H.EBOUND
     assert H.hisparse_pages_compact(p, None) == H.EBOUND
+
+
+@pytest.mark.parametrize("fails", ["*pages.cu*", "*-shared*"])
+def test_a_build_that_fails_leaves_nothing_behind(tmp_path, monkeypatch, fails):
+    """One unit does not compile, or the link fails: the objects go, and so does a half-made library."""
+    exe = tmp_path / "nvcc"
+    exe.write_text('#!/bin/sh\nprev=\nfor a in "$@"; do [ "$prev" = -o ] && : > "$a"; prev=$a; done\n'
+                   f'case "$*" in {fails}) exit 1;; esac\n')
+    exe.chmod(0o755)
+    out = tmp_path / "out" / "lib.so"
+    monkeypatch.setattr(_build, "nvcc", lambda: str(exe))
+    monkeypatch.setattr(_build, "OUT", str(out))
+    with pytest.raises(subprocess.CalledProcessError):
+        _build.build(force=True)
+    assert os.listdir(out.parent) == []
+    assert not [f for f in os.listdir(os.path.join(_build.PKG, "_build")) if f".{os.getpid()}." in f]
+    exe.write_text(exe.read_text().replace("exit 1", "exit 0"))
+    _build.build(force=True)
+    assert os.listdir(out.parent) == ["lib.so"]
