@@ -195,14 +195,15 @@ def pack(rec, k, v, dst, scales, start, *, cu_lens=None, reqs=None, max_len=1, h
     n, R = start.numel(), cs[0]
     _need(reqs is not None or n <= R, "pack: more sequences than requests")
     rows, ds = dst.shape, dst.stride()
-    if dst.dtype is not torch.uint8 or rows[-1] != rec.row_bytes or ds[-1] != 1:
-        raise ValueError("pack: dst is uint8 [..][row_bytes]")
+    if dst.dtype is not torch.uint8 or not 2 <= len(rows) <= 3 or rows[-1] != rec.row_bytes or ds[-1] != 1:
+        raise ValueError("pack: dst is uint8 [rows][row_bytes] or [R][P][row_bytes]")
     req_stride = table = max_blocks = 0
     if len(rows) == 3:
         if rows[0] != R or blocks is not None:
             raise ValueError("pack: dst by position is [R][P][row_bytes], without a page table")
-        # one request, or an expanded one, still goes by position
-        req_stride = ds[0] if R > 1 else max(16, ds[0])
+        if R > 1 and ds[0] == 0:
+            raise ValueError("pack: dst by position has rows of its own for each request")
+        req_stride = ds[0] if R > 1 else max(16, ds[0])  # (one request goes by position too)
     if blocks is not None:
         table, max_blocks = _i32(blocks, "pack: blocks"), blocks.shape[1]
         _need(blocks.shape[0] == R, "pack: blocks is [R][max_blocks]")

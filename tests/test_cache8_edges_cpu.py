@@ -1,4 +1,5 @@
 """What the 8-bit record operators refuse before a launch, beyond test_cache8_cpu.py."""
+import glob
 import os
 import subprocess
 
@@ -67,7 +68,16 @@ def test_a_build_that_fails_leaves_nothing_behind(tmp_path, monkeypatch, fails):
     with pytest.raises(subprocess.CalledProcessError):
         _build.build(force=True)
     assert os.listdir(out.parent) == []
-    assert not [f for f in os.listdir(os.path.join(_build.PKG, "_build")) if f".{os.getpid()}." in f]
+    assert not glob.glob(os.path.join(_build.PKG, "_build", f"*.{os.getpid()}.*"))
     exe.write_text(exe.read_text().replace("exit 1", "exit 0"))
     _build.build(force=True)
     assert os.listdir(out.parent) == ["lib.so"]
+
+
+@pytest.mark.parametrize("dst", [
+    _zeros(1, 1, 3, 256, dtype=torch.uint8), _zeros(256, dtype=torch.uint8),
+    _zeros(1, 3, 256, dtype=torch.uint8).expand(2, 3, 256),
+], ids=["four dimensions", "one", "one request's rows for all"])
+def test_pack_refuses_rows_that_are_neither_by_token_nor_by_position(dst):
+    with pytest.raises(ValueError, match="dst"):
+        _pack(dst=dst, scales=torch.zeros(2, 4, 4))
