@@ -23,6 +23,9 @@ import torch
 from . import hisparse as H
 from .runtime import _stream
 
+# (a third of the time of torch.cuda.current_device, for tensors that CUDA has already)
+_cuda_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
 _DTYPES = {torch.bfloat16: H.BF16, torch.float16: H.F16, torch.float32: H.F32}
 
 
@@ -52,7 +55,7 @@ def _reach(what, first, *others):
     """Raises unless the current CUDA device reads every tensor (or None) where it lies: on that
     device, or in pinned host memory."""
     dev = first.get_device()
-    if dev >= 0 and dev == torch.cuda.current_device():
+    if dev >= 0 and dev == _cuda_device():
         for t in others:
             if t is not None and t.get_device() != dev:
                 break

@@ -41,28 +41,25 @@ class PagePool:
                             _i32(refs, "PagePool: refs", pages), self.work.data_ptr(),
                             _i32(status, "PagePool: status"))
 
-    def _lists(self, what, *named):
-        """The addresses of a call's lists (int32, of one length) and that length, all of them and the
-        pool checked."""
-        n = named[0][1].numel()
-        found = [_i32(t, f"{what}: {name}", n) for name, t in named]
-        _reach(what, self.store, self.tables, self.refs, self.status, *(t for _, t in named))
-        return (*found, n)
-
     def grow(self, reqs, blocks, stream=None):
         """Pages for blocks 0 .. blocks[i]-1 of request reqs[i] (int32, device)."""
-        H.check(H.hisparse_pages_grow(self.c, *self._lists("grow", ("reqs", reqs), ("blocks", blocks)),
-                                      _stream(stream)), "hisparse_pages_grow")
+        n = reqs.numel()
+        d_reqs, d_blocks = _i32(reqs, "grow: reqs"), _i32(blocks, "grow: blocks", n)
+        _reach("grow", self.store, self.tables, self.refs, self.status, reqs, blocks)
+        H.check(H.hisparse_pages_grow(self.c, d_reqs, d_blocks, n, _stream(stream)), "hisparse_pages_grow")
 
     def fork(self, src, dst, tokens, stream=None):
         """Request dst[i] becomes a copy of the first tokens[i] positions of src[i]."""
-        H.check(H.hisparse_pages_fork(self.c, *self._lists("fork", ("src", src), ("dst", dst), ("tokens", tokens)),
-                                      _stream(stream)), "hisparse_pages_fork")
+        n = src.numel()
+        lists = _i32(src, "fork: src"), _i32(dst, "fork: dst", n), _i32(tokens, "fork: tokens", n)
+        _reach("fork", self.store, self.tables, self.refs, self.status, src, dst, tokens)
+        H.check(H.hisparse_pages_fork(self.c, *lists, n, _stream(stream)), "hisparse_pages_fork")
 
     def free(self, reqs, stream=None):
         """Release every page of the listed requests."""
-        H.check(H.hisparse_pages_free(self.c, *self._lists("free", ("reqs", reqs)), _stream(stream)),
-                "hisparse_pages_free")
+        d_reqs = _i32(reqs, "free: reqs")
+        _reach("free", self.store, self.tables, self.refs, self.status, reqs)
+        H.check(H.hisparse_pages_free(self.c, d_reqs, reqs.numel(), _stream(stream)), "hisparse_pages_free")
 
     def compact(self, stream=None):
         """Move the pages in use to the front of the store."""
