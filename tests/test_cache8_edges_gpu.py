@@ -317,3 +317,17 @@ def test_attend_last_page_beyond_the_scale_table(seq, tok, block):
     want = _attend64(rec, c["q"], c["sel"], c["slots"], c["hot"], c["scales"], 64 ** -0.5, tok=tok, seq_lens=lens)
     _attend_close(c["out"], c["lse"], want, torch.bfloat16)
     assert _attend(c, record_tokens=tok) == H.ERR_RANGE      # without lengths they are selected
+
+
+@pytest.mark.parametrize("share", [0.02, 0.5, 1.0])
+@pytest.mark.parametrize("heads,R,n", [(16, 1, 9000), (16, 64, 3001), (128, 2, 700)])
+def test_attend_blocks_without_a_scale_of_v(heads, R, n, share):
+    """Blocks whose V is all 0 have a scale of 0; their tokens have their weight all the same."""
+    c = _attend_case(HEADS, heads, torch.bfloat16, R, 1, n)
+    none = torch.rand(R, c["scales"].shape[1], 1, device="cuda", generator=_gen(n)) < share
+    c["scales"][..., 4:] = c["scales"][..., 4:].masked_fill(none, 0.0)
+    assert _attend(c) == 0
+    some = [0, R - 1] if R > 1 else [0]
+    want = _attend64(HEADS, c["q"][some], c["sel"][some], c["slots"][some], c["hot"][some], c["scales"][some],
+                     128 ** -0.5)
+    _attend_close(c["out"][some], c["lse"][some], want, torch.bfloat16)
