@@ -431,8 +431,9 @@ __device__ __forceinline__ void gather_columns(uint32_t table, uint32_t off, uin
 }
 
 // A tile's columns come, are multiplied and go in two halves: the chunks of K and of V, or those
-// of a latent record in two of about as many 16-byte columns (16 and 20 of 36: 66 us for the largest case,
-// 24 and 12 68).  Chunks [c0, c1) of K or V; the values read [v0, v1) of them.
+// of a latent record in two of about as many 16-byte columns (16 and 20 of 36: 66 us for the largest case
+// with two terms of the probabilities, 24 and 12 68).  Chunks [c0, c1) of K or V; the values read [v0, v1)
+// of them.
 struct Half {
   int c0, c1, v0, v1;
   bool is_v;
@@ -1345,10 +1346,16 @@ struct Plan {
 // distributed shared memory).  A tile's turn is the largest of: its copies, at 27 B/cycle; its
 // products, 32 cycles for the rows and a quarter for each column, 40 at least; the softmax;
 // and the 7,400 cycles from a free stage to the next over the number of stages.  Wider groups read a row
-// fewer times, narrower ones make more CTAs.  For 8 requests of 2048 tokens and 64 heads that
-// reads, against what was measured (us): 16 heads by 4 CTAs 15 (16), 32 by 4 22 (22), 64 by 8
-// 20 (22), 16 by 1 32 (36); for 64 requests of 128 heads: 64 heads by 1 51 (66), 32 by 1 99 (108),
-// 16 by 1 129 (152).
+// fewer times, narrower ones make more CTAs.  What that reads at 1.92 GHz, against what was measured (us,
+// 2048 tokens a row):
+//   8 requests, 64 latent heads: 16 heads by 4 CTAs 16 (16), 32 by 4 22 (22), 64 by 8 20 (22), 16 by 1 37 (35),
+//     16 by 8 38 (36), 32 by 8 33 (34);
+//   32 requests, 32 latent heads: 32 by 4 22 (25), 16 by 2 24 (25), 32 by 2 31 (36), 16 by 1 37 (38), 32 by 1 50 (56);
+//   64 requests, 128 latent heads: 64 by 1 51 (76), 64 by 2 67 (95), 32 by 1 99 (111), 16 by 1 149 (147);
+//   16, 24 and 64 requests, 32 heads on 8 of 128: 16 by 1 20 (22), 40 (42) and 80 (82), by 2 29 (29), 44 (45) and
+//     103 (103), by 4 46 (43) and 68 (65).
+// 64 heads take longer than it says, as two stages are not enough to overlap what a tile goes through; the
+// order is right in each row.
 template <class T, int N>
 int plan_attend(const AttendArgs &args, int64_t pairs, Plan &best) {
   AttendArgs a = args;

@@ -521,7 +521,7 @@ typedef struct {
  * a sin + b cos) at the angle 2pi * frac(d_positions[t] * turns).  Computed in
  * 32 bits and rounded once.  Any strides and alignments of whole elements.
  * Errors: EINVAL (NULL, rot_dim odd or < 2, a rotated part outside the head,
- * unknown type), ECUDA. */
+ * unknown type), EBOUND (rot_dim above 8192, 2^30 values of a token), ECUDA. */
 int hisparse_rotary(const hisparse_rotary_args *args, void *stream);
 
 /* What a record of e4m3 bytes holds.  A token's row is kv_heads K heads of
