@@ -29,10 +29,10 @@
 // addresses and scales, further ahead; and two that issue the products.  S is double buffered in
 // TMEM, so the scores of tile i+1 are computed while the softmax of tile i runs.  A column's offset
 // moves (with its sums and O) only where a probability would exceed 2^15.75, the range of e5m2.  It is set
-// so that 2^12 of that are left above the largest of the warp that lies lowest, and the largest is 2^15 at most:
-// in rows of normal scores the largest of later tiles seldom passes that, and a dominant token gets the
-// whole range below it.  Of 16 requests of 2048 tokens: 21.8 us, 22.6 with 2^10 left and 23.9 with 2^8, 21.4
-// where nothing ever moves.
+// so that 2^12 of that are left above the largest of the warp that lies lowest, and the largest is 2^15 at most
+// and 2^8 at least: in rows of normal scores the largest of later tiles seldom passes that, a dominant token
+// gets the whole range below it, and several of them, one in each warp, what lies below 2^8.  16 requests of
+// 2048 tokens take 22.1 us; 21.6 without the least, 22.5 with 2^10 for it, 21.4 where nothing ever moves.
 //
 // What bounds it, and what it measured.  64 requests of 2048 tokens, 128 heads on one latent head of
 // 576 + 512 (two groups of 64 heads read each row, one from L2): 76 us, where 75 MB of rows would allow 14
@@ -41,8 +41,8 @@
 // 27 B/cycle that 16-byte copies reach on an SM), scores (1150), softmax (2000) and values (1730) overlap
 // only with one other tile's.  (The third product with V is 6 us of it.)  With few rows the fixed parts count: 8
 // requests and 64 heads take 16 us, 6 of them before the first scores (launch, look-up, first rows, cold
-// instructions) and 2 joining clusters; one request of 64 tokens 7.9 us.  16 requests of 8 heads of 128, 32
-// query heads, 2048 tokens (67 MB): 21.7 us, 3.2 TB/s; there a tile's softmax is a chain of waits of one
+// instructions) and 2 joining clusters; one request of 64 tokens 8.2 us.  16 requests of 8 heads of 128, 32
+// query heads, 2048 tokens (67 MB): 22.1 us, 3.1 TB/s; there a tile's softmax is a chain of waits of one
 // warp a scheduler, 1300 cycles.
 // Not kept: rows gathered by the copy engine, four an instruction (100 us where the copies by threads
 // took 100 too); rows prefetched into L2 by the look-up warps (10,000 cycles a tile there); a barrier
@@ -61,10 +61,10 @@ constexpr int kMaxStages = 6;
 constexpr int kMaxCluster = 16;
 constexpr float kNone = -1e30f; // a CTA's offset where it had no token
 constexpr int32_t kMasked = 0x7fffffff;  // in place of K's scale: a token that does not count
-// log2 of a column's largest probability at the most when its offset is set, of what it may grow to
-// before the offset moves again (the largest e5m2 is 57344 = 2^15.8), the room that is left above the
-// warp whose tokens lie lowest, and the largest probability where only one warp has any.
-constexpr float kTop = 15.f, kSlack = 15.75f, kRoom = 12.f, kAlone = 9.f;
+// log2 of a column's largest probability when its offset is set, at the most and at the least; of what it
+// may grow to before the offset moves again (the largest e5m2 is 57344 = 2^15.8); and the room that is left
+// above the warp whose tokens lie lowest.
+constexpr float kTop = 15.f, kLeast = 8.f, kSlack = 15.75f, kRoom = 12.f;
 // Sums of probabilities are kept 2^-kFold of what they are: a token whose scale of V is 2^-100 adds
 // 2^115 at the most, and a few thousand of them would leave the range.
 constexpr float kFold = 16.f;
@@ -754,18 +754,17 @@ __global__ void __launch_bounds__(Shape<N>::threads, 1)
         soft_sync<Shape<N>::groups>(grp);
         if (gt < NC) {
           const int c = c0 + gt;
-          // The largest of the column goes to 2^kTop, or as far below as leaves kRoom above the largest of
-          // the warp that lies lowest: a token far above the others leaves them their bits, and
+          // The largest of the column goes to 2^kTop, or as far below (to 2^kLeast) as leaves kRoom above the
+          // largest of the warp that lies lowest: a token far above the others leaves them their bits, and
           // is not outgrown; one among others leaves room for those that come.
           float m = -INFINITY, low = INFINITY;
-          int warps = 0;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const float x = s_wmax[w][c];
             m = fmaxf(m, x);
-            if (x > -INFINITY) low = fminf(low, x), ++warps;
+            if (x > -INFINITY) low = fminf(low, x);
           }
-          const float top = tiles == 1 ? kTop : warps == 1 ? kAlone : fminf(kTop, kSlack - kRoom + (m - low));
+          const float top = tiles == 1 ? kTop : fminf(kTop, fmaxf(kLeast, kSlack - kRoom + (m - low)));
           const bool fresh = !set && m > -INFINITY;
           const float d = m > kSlack || fresh ? m - top : 0.f;
           s_d[c] = d;

@@ -521,7 +521,7 @@ typedef struct {
  * a sin + b cos) at the angle 2pi * frac(d_positions[t] * turns).  Computed in
  * 32 bits and rounded once.  Any strides and alignments of whole elements.
  * Errors: EINVAL (NULL, rot_dim odd or < 2, a rotated part outside the head,
- * unknown type), EBOUND (rot_dim above 8192, 2^30 values of a token), ECUDA. */
+ * unknown type), EBOUND (rot_dim above 8192; from 2^24 values of a token on), ECUDA. */
 int hisparse_rotary(const hisparse_rotary_args *args, void *stream);
 
 /* What a record of e4m3 bytes holds.  A token's row is kv_heads K heads of
@@ -626,7 +626,7 @@ typedef struct {
  * cores as the e4m3 they are, q and the products p * sV of a probability and its scale of V as sums of
  * 8-bit terms.  q is exact down to 2^-9 (f16: 2^-6) of the head's largest value, and within 2^-17 of that
  * below.  p * sV is within 2^-11 (f16: 2^-15) of itself, or, if that is more, within 2^-32 of the largest
- * where a token stands out (by 2^12 from those beside it), and at worst within 2^-20 of it.
+ * where one token stands out (by 2^12 from those beside it), and at worst within 2^-25 of it.
  * A scale of V below 2^-100 counts as 2^-100.
  * A NaN scale of K gives NaN in out and lse of the rows that read it; one of V that is NaN or
  * infinite in out alone.  A slot

@@ -231,37 +231,32 @@ def test_attend_infinite_scales_of_k():
     _attend_close(c["out"][low][None, None], c["lse"][low][None, None], [x[m][None, None] for x in want], torch.bfloat16)
 
 
-@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("rec,heads,R,at", [
-    (LATENT, 128, 1, 0), (LATENT, 128, 80, 5), (LATENT, 16, 160, 2040), (LATENT, 64, 2, 700),
-    (HEADS, 16, 40, 0), (HEADS, 16, 1, 1300), (HEADS, 128, 1, 0), (cache8.Records(2, 64, 64, 32), 6, 160, 1),
-])
-@pytest.mark.parametrize("weight", [0.5, 0.95, 0.997, 0.9999])
-def test_attend_beside_a_dominant_token_without_values(rec, heads, R, at, weight, dtype):
-    """One token has most of the weight and a V of 0, so that the output is made of the others'
-    small probabilities.  Its error is bounded by itself: the rounding of the output (at most
-    U / 3^0.5 of its norm, 2^-25 a value at the lower end of f16) with half as much again, 2^-11 of each
-    probability, and 2^-32 of the largest probability times its scale of V (half as much again over
-    3^0.5), by the norm of V's bytes."""
+def _beside_dominant_tokens(rec, heads, R, at, weight, dtype, floor):
+    """Rows of 2048 tokens of which those of entries `at` have `weight` together and a V of 0, so that
+    the output is made of the others' small probabilities.  Its error is bounded by itself: the rounding of
+    the output (at most U / 3^0.5 of its norm, 2^-25 a value at the lower end of f16) with half as much
+    again, 2^-11 of each probability, and `floor` of the largest probability times its scale of V (half as
+    much again over 3^0.5), by the norm of V's bytes."""
     n, D, K = 2048, rec.k_dim, rec.kv_heads
     c = _attend_case(rec, heads, dtype, R, 1, n, pad=0.0)
     hot, scales = c["hot"].view(E4M3), c["scales"]
     far = torch.arange(K, device="cuda") * D + D - 1
     hot[..., far] = torch.tensor(0.0, device="cuda").to(E4M3)
     c["q"][..., D - 1] = 1.0
-    slot = c["slots"][:, at].long()
-    hot[torch.arange(R, device="cuda"), slot] = torch.tensor(0.0, device="cuda").to(E4M3)
-    for f in far.tolist():
-        hot[torch.arange(R, device="cuda"), slot, f] = torch.tensor(448.0, device="cuda").to(E4M3)
-    # a block of its own, whose scale makes its score what the weight asks for
+    # a block of their own, whose scale makes their scores what the weight asks for
     blk = scales.shape[1]
-    c["sel"][:, at] = blk * rec.block_tokens
+    for i, entry in enumerate(at):
+        slot = c["slots"][:, entry].long()
+        hot[torch.arange(R, device="cuda"), slot] = torch.tensor(0.0, device="cuda").to(E4M3)
+        for f in far.tolist():
+            hot[torch.arange(R, device="cuda"), slot, f] = torch.tensor(448.0, device="cuda").to(E4M3)
+        c["sel"][:, entry] = blk * rec.block_tokens + i
     c["scales"] = torch.cat([scales, torch.full((R, 1, rec.columns), 1 / 60, device="cuda")], 1).contiguous()
     some = [0, R - 1] if R > 1 else [0]
     pick = lambda: _attend64(rec, c["q"][some], c["sel"][some], c["slots"][some], c["hot"][some], c["scales"][some], D ** -0.5)
     c["scales"][:, blk, :K] = -50.0
     rest = float(np.median(pick()[1]))                    # lse of the others
-    c["scales"][:, blk, :K] = (rest + np.log(weight / (1 - weight))) * D ** 0.5 / 448
+    c["scales"][:, blk, :K] = (rest + np.log(weight / (1 - weight) / len(at))) * D ** 0.5 / 448
     assert _attend(c) == 0
     want, lse, _, _ = pick()
     got = c["out"][some].double().cpu().numpy()
@@ -272,8 +267,28 @@ def test_attend_beside_a_dominant_token_without_values(rec, heads, R, at, weight
     norm_v = float(bytes_v.double().norm(dim=(1, 2)).max()) / (1 if rec.latent else K ** 0.5)
     s_v = float(c["scales"][:, blk, 0 if rec.latent else K].max())
     low = 0.0 if dtype is torch.bfloat16 else 2.0 ** -25 * rec.v_dim ** 0.5 / size
-    tol = 1.5 * (U[dtype] + low) / 3 ** 0.5 + 2.0 ** -11 + 1.5 * 2.0 ** -32 / 3 ** 0.5 * weight * s_v * norm_v / size
+    tol = 1.5 * (U[dtype] + low) / 3 ** 0.5 + 2.0 ** -11 \
+        + 1.5 * floor / 3 ** 0.5 * weight / len(at) * s_v * norm_v / size
     assert (err <= tol).all(), (float((err / tol).max()), float(err.max()), float(tol.min()))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rec,heads,R,at", [
+    (LATENT, 128, 1, 0), (LATENT, 128, 80, 5), (LATENT, 16, 160, 2040), (LATENT, 64, 2, 700),
+    (HEADS, 16, 40, 0), (HEADS, 16, 1, 1300), (HEADS, 128, 1, 0), (cache8.Records(2, 64, 64, 32), 6, 160, 1),
+])
+@pytest.mark.parametrize("weight", [0.5, 0.95, 0.997, 0.9999])
+def test_attend_beside_a_dominant_token_without_values(rec, heads, R, at, weight, dtype):
+    """One token far above the others of its tile."""
+    _beside_dominant_tokens(rec, heads, R, [at], weight, dtype, 2.0 ** -32)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rec,heads,R", [(HEADS, 16, 40), (HEADS, 16, 1), (cache8.Records(1, 128, 128, 64), 64, 160)])
+@pytest.mark.parametrize("weight", [0.9, 0.997])
+def test_attend_beside_dominant_tokens_in_every_warp(rec, heads, R, weight, dtype):
+    """Several, so placed in the first tile that each warp has one and none stands out."""
+    _beside_dominant_tokens(rec, heads, R, [3, 35, 67, 99], weight, dtype, 2.0 ** -25)
 
 
 @pytest.mark.parametrize("rec,heads", [(HEADS, 16), (cache8.Records(1, 128, 128, 16), 64)])
